@@ -223,6 +223,147 @@ SIGATTN_API int sigattn_bwd_dkdv_varlen(const void* q, const void* k, const void
                                         void* dv, const int32_t* cu_seqlens, int B, int H, int max_seqlen, int total,
                                         int d, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving from a paged cache: the keys and values of earlier tokens stay in
+ * fixed-size pages, and each call attends with a chunk of new tokens (a whole
+ * prompt, part of one, or a single token per sequence; any mixture in one
+ * batch). A step is: sigattn_paged_reserve (pages and slots for the new
+ * tokens), sigattn_paged_write (rotate and store them), sigattn_fwd_paged
+ * (attend), and when a request ends or tokens are taken back
+ * sigattn_paged_release. All bookkeeping stays on the device, so a step can be
+ * captured into a CUDA graph and replayed.
+ *
+ * Conventions of the paged calls
+ *  - k_cache, v_cache: [num_pages][Hkv][page_size][d] bf16, contiguous, 16-byte
+ *    aligned; d is 64 or 128, page_size 16, 32, 64, 128 or 256. Slot s is row
+ *    s % page_size of page s / page_size; num_pages * page_size and num_pages
+ *    * Hkv may not exceed INT32_MAX.
+ *  - block_table: int32 [B][max_pages]; entry k of row b is the page that holds
+ *    tokens [k * page_size, (k + 1) * page_size) of sequence b. Entries past
+ *    a sequence's pages are not read. max_pages * page_size <=
+ *    SIGATTN_MAX_PAGED_LEN.
+ *  - Hq query heads share Hkv key/value heads: Hq = G * Hkv, and query head h
+ *    reads key/value head h / G; G <= 128.
+ *  - cu_seqlens: int32 [B+1] as in the packed layout: the new tokens of
+ *    sequence b are rows cu_seqlens[b] .. cu_seqlens[b+1]-1. kv_lens: int32
+ *    [B], the tokens of sequence b in the cache, its new ones included.
+ *  - q, k, v, q_out are rows of [heads][d] bf16 with a stride between tokens
+ *    (in elements, a multiple of 8, >= heads * d), so that they may be slices
+ *    of one fused projection; 16-byte aligned.
+ *  - workspace: 16-byte aligned, zeroed once, with the sticky error word of
+ *    every call; sigattn_paged_workspace_size bytes for sigattn_fwd_paged and
+ *    256 bytes for the others. Calls that may run concurrently need
+ *    different workspaces. The calls leave their own counters there at zero;
+ *    after SIGATTN_ERR_TIMEOUT zero the workspace again (sigattn_read_error
+ *    does that for its header).
+ *  - 1 <= B <= SIGATTN_MAX_BATCH. Values found to be bad on the device raise
+ *    SIGATTN_ERR_INVALID_ARG in the sticky error word, as stated at each call;
+ *    nothing out of bounds is ever read or written. */
+#define SIGATTN_MAX_PAGED_LEN (1 << 24)
+
+/* Take pages for new tokens: sequence b has cached_lens[b] tokens and gets
+ * new_lens[b] more. Its first ceil(cached / page_size) table entries are in
+ * use; the further pages that cached + new tokens need are popped from the
+ * stack free_pages[0 .. *free_count), top first, in batch order (sequence 0's
+ * first page is the top), and written to its row of block_table.
+ * Written besides (int32, on the device):
+ *  - cu_seqlens [B+1]: exclusive prefix sums of new_lens;
+ *  - kv_lens [B]: cached + new (may be the same array as cached_lens);
+ *  - slots [rows]: each new token's slot, in cu_seqlens order; rows at or past
+ *    cu_seqlens[B] get -1 (which sigattn_paged_write skips), so a captured
+ *    step may carry a padded number of rows;
+ *  - positions [rows] (optional, NULL to omit): each new token's position in
+ *    its sequence, cached + 0, 1, ...; rows past the last get 0;
+ *  - *free_count_out: the pages left (may be the same word as free_count).
+ * num_pages is the capacity of free_pages and the bound on page numbers.
+ * The request is met whole or not at all. If a length is negative, a
+ * sequence would exceed max_pages * page_size tokens, the new tokens exceed
+ * `rows`, or the stack holds too few pages, then the error word is raised
+ * (site -(b+1) for a sequence's length, 201 for rows, 202 for pages), the table
+ * and the stack stay as they were, cu_seqlens is all zero, kv_lens is
+ * cached_lens, slots are -1 and *free_count_out is *free_count. A page number
+ * outside [0, num_pages) in the stack or the table raises site 203; its tokens
+ * get slot -1. */
+SIGATTN_API int sigattn_paged_reserve(const int32_t* cached_lens, const int32_t* new_lens, int32_t* block_table,
+                                      const int32_t* free_pages, const int32_t* free_count, int32_t* free_count_out,
+                                      int32_t* cu_seqlens, int32_t* kv_lens, int32_t* slots, int32_t* positions, int B,
+                                      int max_pages, int page_size, int num_pages, int rows, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* Give pages back: sequence b holds kv_lens[b] tokens and keeps the first
+ * keep_lens[b] (keep_lens NULL: none). Its pages [ceil(keep / page_size),
+ * ceil(kv / page_size)) are pushed on the stack in batch order, each sequence's
+ * in order of position, and *free_count_out is the new height (may be the same
+ * word as free_count). block_table and kv_lens are not changed. If a length is
+ * bad (0 <= keep <= kv <= max_pages * page_size is broken: site -(b+1)) or the
+ * stack would exceed num_pages (site 202), nothing is pushed and
+ * *free_count_out is *free_count. A page number outside [0, num_pages) in the
+ * table is pushed as -1 and raises site 203. */
+SIGATTN_API int sigattn_paged_release(const int32_t* kv_lens, const int32_t* keep_lens, const int32_t* block_table,
+                                      int32_t* free_pages, const int32_t* free_count, int32_t* free_count_out, int B,
+                                      int max_pages, int page_size, int num_pages, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* Store new keys and values in their slots and, with rotary positions, turn
+ * the keys (and queries) on the way. k, v: `rows` rows of [Hkv][d]; row t goes to
+ * slot slots[t] of k_cache and v_cache; slot -1 stores nothing (another slot
+ * outside the cache stores nothing and raises site 204). Slots other than -1
+ * must be distinct: which row a repeated slot ends up with is not defined.
+ *  - q, q_out (both or neither; `rows` rows of [Hq][d], any Hq >= 1): q_out
+ *    receives the turned queries of every row, whatever its slot; q_out may
+ *    be q itself (same stride).
+ *  - Rotary positions: `pairs` > 0 pairs of values of each head are turned
+ *    (a multiple of 8, 2 * pairs <= d; 0: none, values are copied). Pair i is
+ *    values (i, i + pairs), or with `adjacent` (2i, 2i + 1), and becomes
+ *    (x1 cos a - x2 sin a, x2 cos a + x1 sin a) with a = p * inv_freq[i], where
+ *    p = positions[pair_axis[i]][t] (int32 [axes][rows]; pair_axis int32
+ *    [pairs], NULL: all pairs turn with axis 0). Several axes give image and
+ *    video tokens their time, height and width. inv_freq: fp32 [pairs].
+ *    Values past 2 * pairs are copied. The angle is formed and reduced in 64
+ *    bits, so far positions lose nothing; the turn is computed in fp32 and
+ *    rounded once. An axis outside [0, axes) counts as 0 and raises site 205.
+ *  - k, v, q must not overlap the caches. */
+SIGATTN_API int sigattn_paged_write(const void* k, long long k_stride, const void* v, long long v_stride,
+                                    const int32_t* slots, void* k_cache, void* v_cache, const void* q,
+                                    long long q_stride, void* q_out, long long q_out_stride, const int32_t* positions,
+                                    const float* inv_freq, const int32_t* pair_axis, int axes, int pairs, int adjacent,
+                                    int rows, int Hq, int Hkv, int d, int page_size, int num_pages, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for sigattn_fwd_paged: a 256-byte header and room for
+ * the partial sums of rows whose keys are split over several SMs (does not
+ * depend on the batch or on lengths). Returns 0 if the sizes are out of range. */
+SIGATTN_API size_t sigattn_paged_workspace_size(int Hq, int Hkv, int d, int max_seqlen_q);
+
+/* Sigmoid attention of a chunk of new tokens over the paged cache. Row i of
+ * sequence b's q_b = cu_seqlens[b+1] - cu_seqlens[b] new tokens stands at
+ * position p = kv_lens[b] - q_b + i of its sequence and sees N keys: the first
+ * p + 1 with `causal`, else all kv_lens[b];
+ *     o_i = sum_{j < N} sigma(q_i . k_j / sqrt(d) - ln N) v_j.
+ * The bias counts the keys that the row sees, so a causal row's result does
+ * not depend on how its prompt was cut into chunks, and with causal = 0 and
+ * nothing cached before it is sigattn_fwd_varlen's. A row that sees no key
+ * (kv_lens[b] = 0, or p < 0 where more rows than tokens are given) is zero.
+ *  - q: `total` rows of [Hq][d]; o: [total][Hq][d] bf16, contiguous. Rows
+ *    outside every [cu_seqlens[b], cu_seqlens[b+1]) are never written.
+ *  - max_seqlen_q >= every q_b (kernel choice, limits). kv_lens[b] <= max_pages
+ *    * page_size. A sequence that breaks these rules, or whose cu_seqlens
+ *    bounds are out of order or out of [0, total], gets no work: its rows are
+ *    left untouched and the error word is raised (site -(b+1)).
+ *  - A page number outside [0, num_pages) among a sequence's pages contributes
+ *    nothing to its sums and raises site 203.
+ *  - Cached values of tokens < kv_lens[b] must be finite; whatever else the
+ *    pages hold (NaN included) changes no result.
+ *  - The keys are cut over the SMs where that balances the work, and the
+ *    fp32 partial sums are added in a fixed order: no atomics touch a result,
+ *    and a repeated call gives the same bits.
+ *  - Arithmetic as sigattn_fwd. One launch. Forward only. */
+SIGATTN_API int sigattn_fwd_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, void* o,
+                                  const int32_t* cu_seqlens, const int32_t* kv_lens, const int32_t* block_table, int B,
+                                  int Hq, int Hkv, int max_seqlen_q, int total, int max_pages, int page_size,
+                                  int num_pages, int d, int causal, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
 /* Run only the ragged tile scheduler for `kind` on the device: afterwards the
  * workspace holds, at byte offset 8, the item count (int32), and at byte
  * offset 256, `count` entries of four int32 (bh = b*H + h, block index, the

@@ -26,6 +26,8 @@ __all__ = [
     "sigattn_fwd_varlen", "sigattn_bwd_varlen", "sigattn_bwd_dq_varlen", "sigattn_bwd_dkdv_varlen",
     "sigattn_fwd_partial", "sigattn_bwd_dq_partial", "sigattn_bwd_dkdv_range", "sigattn_cast_bf16",
     "sigattn_softmax_fwd",
+    "sigattn_paged_reserve", "sigattn_paged_release", "sigattn_paged_write", "sigattn_paged_workspace_size",
+    "sigattn_fwd_paged", "PagedCache",
     "KIND_FWD", "KIND_DQ", "KIND_DKDV", "SigmoidAttentionFunction", "sigmoid_attention",
     "SigmoidAttentionVarlenFunction", "sigmoid_attention_varlen",
 ]
@@ -41,6 +43,7 @@ _lib = None
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
+_ll = ctypes.c_longlong
 
 
 class SigattnError(RuntimeError):
@@ -104,6 +107,17 @@ def library():
         lib.sigattn_bwd_dkdv_range.argtypes = [_vp] * 7 + [_i] * 6 + [_vp, _sz, _vp]
         lib.sigattn_softmax_fwd.restype = _i
         lib.sigattn_softmax_fwd.argtypes = [_vp] * 5 + [_i] * 4 + [_vp, _sz, _vp]
+        lib.sigattn_paged_reserve.restype = _i
+        lib.sigattn_paged_reserve.argtypes = [_vp] * 10 + [_i] * 5 + [_vp, _sz, _vp]
+        lib.sigattn_paged_release.restype = _i
+        lib.sigattn_paged_release.argtypes = [_vp] * 6 + [_i] * 4 + [_vp, _sz, _vp]
+        lib.sigattn_paged_write.restype = _i
+        lib.sigattn_paged_write.argtypes = [_vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp, _ll, _vp, _ll, _vp, _vp, _vp] + [
+            _i] * 9 + [_vp, _sz, _vp]
+        lib.sigattn_paged_workspace_size.restype = _sz
+        lib.sigattn_paged_workspace_size.argtypes = [_i] * 4
+        lib.sigattn_fwd_paged.restype = _i
+        lib.sigattn_fwd_paged.argtypes = [_vp, _ll] + [_vp] * 6 + [_i] * 10 + [_vp, _sz, _vp]
         lib.sigattn_cast_bf16.restype = _i
         lib.sigattn_cast_bf16.argtypes = [_vp, _vp, ctypes.c_longlong, _vp]
         lib.sigattn_eval_sigmoid.restype = _i
@@ -299,6 +313,148 @@ def sigattn_bwd_dkdv_varlen(q, k, v, dout, dk, dv, cu_seqlens, max_seqlen: int, 
         _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream_ptr(stream)))
 
 
+# ---------------------------------------------------------------------------
+# Serving from a paged cache (see the C header for the conventions)
+# ---------------------------------------------------------------------------
+def _rows(t: torch.Tensor, name: str, heads: int = 0, d: int = 0) -> int:
+    """Pointer of a [rows, heads, d] bf16 tensor whose rows may be strided
+    (slices of one fused projection)."""
+    if t.dim() != 3 or not t.is_cuda or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a [rows, heads, d] CUDA torch.bfloat16 tensor")
+    if (t.stride(2) != 1 and t.shape[2] > 1) or (t.stride(1) != t.shape[2] and t.shape[1] > 1):
+        raise ValueError(f"{name} must be contiguous within each row")
+    if (heads and t.shape[1] != heads) or (d and t.shape[2] != d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [rows, {heads or t.shape[1]}, {d or t.shape[2]}]")
+    return t.data_ptr()
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _same_device(first: torch.Tensor, **others) -> None:
+    """All tensors on one device, which must be the current one (the library
+    launches on the current device)."""
+    if first.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {first.device}, the current device is cuda:{torch.cuda.current_device()}")
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+
+
+def _int32(t: torch.Tensor, name: str, *shape: int) -> int:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    return _dev(t, name, torch.int32)
+
+
+def _cache_dims(k_cache: torch.Tensor, v_cache: torch.Tensor):
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must be [num_pages, Hkv, page_size, d] tensors of one shape")
+    return tuple(k_cache.shape)
+
+
+def sigattn_paged_reserve(cached_lens, new_lens, block_table, free_pages, free_count, free_count_out, cu_seqlens,
+                          kv_lens, slots, positions, page_size: int, workspace, stream=None) -> None:
+    """Take pages for new_lens[b] more tokens of every sequence and write
+    cu_seqlens, kv_lens, slots and positions (None to omit) for them."""
+    B = cached_lens.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    _same_device(cached_lens, new_lens=new_lens, block_table=block_table, free_pages=free_pages, free_count=free_count,
+                 free_count_out=free_count_out, cu_seqlens=cu_seqlens, kv_lens=kv_lens, slots=slots,
+                 positions=positions, workspace=workspace)
+    rows = slots.numel()
+    _check("sigattn_paged_reserve", library().sigattn_paged_reserve(
+        _int32(cached_lens, "cached_lens", B), _int32(new_lens, "new_lens", B),
+        _int32(block_table, "block_table", B, block_table.shape[1]), _dev(free_pages, "free_pages", torch.int32),
+        _int32(free_count, "free_count", 1), _int32(free_count_out, "free_count_out", 1),
+        _int32(cu_seqlens, "cu_seqlens", B + 1), _int32(kv_lens, "kv_lens", B), _int32(slots, "slots", rows),
+        None if positions is None else _int32(positions, "positions", rows), B, block_table.shape[1], int(page_size),
+        free_pages.numel(), rows, _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream_ptr(stream)))
+
+
+def sigattn_paged_release(kv_lens, keep_lens, block_table, free_pages, free_count, free_count_out, page_size: int,
+                          workspace, stream=None) -> None:
+    """Push the pages past each sequence's first keep_lens[b] tokens (None: all
+    pages) back on the stack of free pages."""
+    B = kv_lens.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    _same_device(kv_lens, keep_lens=keep_lens, block_table=block_table, free_pages=free_pages, free_count=free_count,
+                 free_count_out=free_count_out, workspace=workspace)
+    _check("sigattn_paged_release", library().sigattn_paged_release(
+        _int32(kv_lens, "kv_lens", B), None if keep_lens is None else _int32(keep_lens, "keep_lens", B),
+        _int32(block_table, "block_table", B, block_table.shape[1]), _dev(free_pages, "free_pages", torch.int32),
+        _int32(free_count, "free_count", 1), _int32(free_count_out, "free_count_out", 1), B, block_table.shape[1],
+        int(page_size), free_pages.numel(), _dev(workspace, "workspace", torch.uint8), workspace.numel(),
+        _stream_ptr(stream)))
+
+
+def sigattn_paged_write(k, v, slots, k_cache, v_cache, workspace, q=None, q_out=None, positions=None, inv_freq=None,
+                        pair_axis=None, adjacent: bool = False, stream=None) -> None:
+    """Store the rows of k and v ([rows, Hkv, d]) in their slots. With inv_freq
+    (fp32 [pairs]) the keys, and q into q_out, are turned by positions
+    (int32 [rows] or [axes, rows]; pair_axis int32 [pairs] names each pair's
+    axis)."""
+    pages, Hkv, ps, d = _cache_dims(k_cache, v_cache)
+    rows = k.shape[0]
+    _same_device(k_cache, v_cache=v_cache, k=k, v=v, slots=slots, workspace=workspace, q=q, q_out=q_out,
+                 positions=positions, inv_freq=inv_freq, pair_axis=pair_axis)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    kp, vp = _rows(k, "k", Hkv, d), _rows(v, "v", Hkv, d)
+    if v.shape[0] != rows:
+        raise ValueError("k and v must have the same number of rows")
+    qp = qo = None
+    Hq = qs = qos = 0
+    if q is not None:
+        Hq = q.shape[1]
+        qp, qo, qs, qos = _rows(q, "q", Hq, d), _rows(q_out, "q_out", Hq, d), _row_stride(q), _row_stride(q_out)
+        if q.shape[0] != rows or q_out.shape[0] != rows:
+            raise ValueError("q and q_out must have k's number of rows")
+    pp = fp = ap = None
+    pairs, axes = 0, 1
+    if inv_freq is not None:
+        if positions is None:
+            raise ValueError("rotary positions need positions and inv_freq")
+        pairs = inv_freq.numel()
+        fp = _dev(inv_freq, "inv_freq", torch.float32)
+        axes = 1 if positions.dim() == 1 else positions.shape[0]
+        pp = _int32(positions, "positions", *((rows,) if positions.dim() == 1 else (axes, rows)))
+        ap = None if pair_axis is None else _int32(pair_axis, "pair_axis", pairs)
+    _check("sigattn_paged_write", library().sigattn_paged_write(
+        kp, _row_stride(k), vp, _row_stride(v), _int32(slots, "slots", rows), _dev(k_cache, "k_cache"),
+        _dev(v_cache, "v_cache"), qp, qs, qo, qos, pp, fp, ap, axes, pairs, int(bool(adjacent)), rows, Hq, Hkv, d, ps,
+        pages, _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream_ptr(stream)))
+
+
+def sigattn_paged_workspace_size(Hq: int, Hkv: int, d: int, max_seqlen_q: int) -> int:
+    return library().sigattn_paged_workspace_size(Hq, Hkv, d, max_seqlen_q)
+
+
+def sigattn_fwd_paged(q, k_cache, v_cache, o, cu_seqlens, kv_lens, block_table, max_seqlen_q: int, causal: bool,
+                      workspace, stream=None) -> None:
+    """Attention of the new tokens' q ([total, Hq, d], rows may be strided) over
+    the cached keys and values; o is [total, Hq, d]."""
+    pages, Hkv, ps, d = _cache_dims(k_cache, v_cache)
+    qp = _rows(q, "q", 0, d)
+    total, Hq = q.shape[0], q.shape[1]
+    if tuple(o.shape) != (total, Hq, d):
+        raise ValueError("o must have q's shape")
+    B = kv_lens.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    _same_device(k_cache, v_cache=v_cache, q=q, o=o, cu_seqlens=cu_seqlens, kv_lens=kv_lens, block_table=block_table,
+                 workspace=workspace)
+    _check("sigattn_fwd_paged", library().sigattn_fwd_paged(
+        qp, _row_stride(q), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(o, "o"),
+        _int32(cu_seqlens, "cu_seqlens", B + 1), _int32(kv_lens, "kv_lens", B),
+        _int32(block_table, "block_table", B, block_table.shape[1]), B, Hq, Hkv, int(max_seqlen_q), total,
+        block_table.shape[1], ps, pages, d, int(bool(causal)), _dev(workspace, "workspace", torch.uint8),
+        workspace.numel(), _stream_ptr(stream)))
+
+
 def sigattn_plan(lengths, B, H, Lmax, d, kind, workspace, stream=None) -> None:
     _check("sigattn_plan", library().sigattn_plan(
         _dev(lengths, "lengths", torch.int32), B, H, Lmax, d, kind, _dev(workspace, "workspace", torch.uint8),
@@ -451,3 +607,69 @@ def sigmoid_attention_varlen(q, k, v, cu_seqlens, max_seqlen: int, check: bool =
     """The packed-layout counterpart of ``sigmoid_attention`` ([total, H, d]
     tensors, int32 cu_seqlens [B + 1]); ``check`` as there."""
     return SigmoidAttentionVarlenFunction.apply(q, k, v, cu_seqlens, int(max_seqlen), check)
+
+
+class PagedCache:
+    """Keys and values of up to ``batch`` running sequences in ``num_pages``
+    pages of ``page_size`` tokens, with the bookkeeping on the device.
+
+    ``step`` admits new tokens of every sequence (any number each, none
+    included), stores them and attends; ``release`` takes tokens back or ends
+    sequences. Nothing synchronises, so a step can be captured into a CUDA
+    graph (make one call outside the capture first); ``check`` reads the sticky
+    error word."""
+
+    def __init__(self, num_pages: int, page_size: int, Hq: int, Hkv: int, d: int, batch: int, max_pages: int,
+                 max_new: int = 1, device=None):
+        device = torch.device(device or "cuda")
+        z = lambda *s: torch.zeros(s, dtype=torch.int32, device=device)  # noqa: E731
+        size = sigattn_paged_workspace_size(Hq, Hkv, d, max_new)
+        if size == 0:
+            raise SigattnError("sigattn_paged_workspace_size", 2)
+        self.page_size, self.max_new = page_size, max_new
+        self.k = torch.zeros(num_pages, Hkv, page_size, d, dtype=torch.bfloat16, device=device)
+        self.v = torch.zeros_like(self.k)
+        self.block_table, self.lens, self.cu_seqlens = z(batch, max_pages), z(batch), z(batch + 1)
+        # pages are popped from the end of the stack: page 0 first
+        self.free_pages = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        self.free_count = torch.full((1,), num_pages, dtype=torch.int32, device=device)
+        self.workspace = torch.zeros(size, dtype=torch.uint8, device=device)
+
+    def step(self, q, k, v, new_lens, causal: bool = True, positions=None, inv_freq=None, pair_axis=None,
+             adjacent: bool = False) -> torch.Tensor:
+        """Rows of q ([rows, Hq, d]), k and v ([rows, Hkv, d]) are the new
+        tokens, new_lens[b] (at most ``max_new``) of sequence b, in batch
+        order; rows past them are ignored (their output rows are zero). With
+        inv_freq, q and k are turned first, by ``positions`` or by each
+        token's place in its sequence. Returns [rows, Hq, d]."""
+        rows = q.shape[0]
+        slots = torch.empty(rows, dtype=torch.int32, device=q.device)
+        places = torch.empty_like(slots)
+        sigattn_paged_reserve(self.lens, new_lens, self.block_table, self.free_pages, self.free_count, self.free_count,
+                              self.cu_seqlens, self.lens, slots, places, self.page_size, self.workspace)
+        if inv_freq is None:
+            sigattn_paged_write(k, v, slots, self.k, self.v, self.workspace)
+        else:
+            turned = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            sigattn_paged_write(k, v, slots, self.k, self.v, self.workspace, q=q, q_out=turned,
+                                positions=places if positions is None else positions, inv_freq=inv_freq,
+                                pair_axis=pair_axis, adjacent=adjacent)
+            q = turned
+        o = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+        sigattn_fwd_paged(q, self.k, self.v, o, self.cu_seqlens, self.lens, self.block_table, self.max_new, causal,
+                          self.workspace)
+        return o
+
+    def release(self, keep_lens=None) -> None:
+        """Keep the first keep_lens[b] tokens of every sequence (None: none)
+        and give the other pages back."""
+        sigattn_paged_release(self.lens, keep_lens, self.block_table, self.free_pages, self.free_count, self.free_count,
+                              self.page_size, self.workspace)
+        if keep_lens is None:
+            self.lens.zero_()
+        else:
+            self.lens.copy_(keep_lens)
+
+    def check(self) -> None:
+        """Synchronise and raise if a call reported a problem on the device."""
+        _check_device_status("PagedCache", self.workspace, True)

@@ -9,7 +9,7 @@
 #include <mutex>
 
 #include "../../include/sigattn.h"
-#include "common.cuh"
+#include "paged.cuh"
 
 namespace sigattn {
 cudaError_t launch_prep(const int* lengths, const int* cu, int total, int B, int H, int L, int kind, KeyRange kr,
@@ -36,6 +36,10 @@ cudaError_t launch_bwd_dkdv(int d, bool packed, const CUtensorMap& tk, const CUt
                             const CUtensorMap& tdo, void* dk, void* dv, int* ws, int B, int H, int out_rows, int Lmax,
                             KeyRange kr, int num_sms, const int* fill_lengths, cudaStream_t stream,
                             const BwdLink& link = BwdLink{});
+cudaError_t launch_paged_reserve(const PagedReserve& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_paged_release(const PagedRelease& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_paged_write(PagedWrite a, int num_sms, cudaStream_t stream);
+cudaError_t launch_fwd_paged(const PagedAttend& a, int num_sms, cudaStream_t stream);
 void set_last_error(const char* msg);
 }  // namespace sigattn
 
@@ -159,6 +163,47 @@ int cuda_status(cudaError_t e) {
 void sigattn::set_last_error(const char* msg) { snprintf(g_last_error, sizeof(g_last_error), "%s", msg); }
 
 namespace {
+
+constexpr size_t kHeaderBytes = static_cast<size_t>(kHeaderWords) * 4;
+constexpr int kMaxWriteHeads = 4096;  // Hq + 2 Hkv of a cache write
+
+bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Batch and page geometry of a paged call; *shift receives log2(page_size).
+int check_pages(int B, int max_pages, int page_size, int num_pages, int* shift) {
+  if (B < 1 || max_pages < 1 || num_pages < 1) return SIGATTN_ERR_INVALID_ARG;
+  if (B > kMaxBatch) return SIGATTN_ERR_UNSUPPORTED;
+  for (*shift = 4; *shift <= 8; ++*shift)
+    if (page_size == 1 << *shift) break;
+  if (*shift > 8) return SIGATTN_ERR_UNSUPPORTED;
+  if (max_pages > kMaxPagedLen >> *shift || num_pages > INT_MAX >> *shift) return SIGATTN_ERR_UNSUPPORTED;
+  return SIGATTN_OK;
+}
+
+bool cache_fits(int num_pages, int Hkv) { return static_cast<long long>(num_pages) * Hkv <= INT_MAX; }
+
+// A token stride (in elements) that keeps rows of [heads][d] apart and 16-byte aligned.
+bool row_stride_ok(long long stride, int heads, int d) {
+  return stride % 8 == 0 && stride >= static_cast<long long>(heads) * d && stride <= (1LL << 36);
+}
+
+// Head counts and size of sigattn_fwd_paged.
+int check_paged_heads(int Hq, int Hkv, int d) {
+  if (d != 64 && d != 128) return SIGATTN_ERR_UNSUPPORTED;
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return SIGATTN_ERR_INVALID_ARG;
+  if (Hq / Hkv > kMaxPagedGroup || Hq > (1 << 20)) return SIGATTN_ERR_UNSUPPORTED;
+  return SIGATTN_OK;
+}
+
+// The workspace and device checks of a paged call.
+int check_paged_call(const void* ws, size_t ws_bytes, size_t need, DeviceInfo* info) {
+  if (!aligned16(ws) || ws_bytes < need) return SIGATTN_ERR_INVALID_ARG;
+  if (!device_info(info)) {
+    const cudaError_t e = cudaGetLastError();
+    return cuda_status(e != cudaSuccess ? e : cudaErrorUnknown);
+  }
+  return info->supported ? SIGATTN_OK : SIGATTN_ERR_UNSUPPORTED;
+}
 
 int map_failure() {
   snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled failed or is unavailable");
@@ -508,6 +553,131 @@ int sigattn_bwd_dkdv_varlen(const void* q, const void* k, const void* v, const v
   if (st != SIGATTN_OK) return st;
   return cuda_status(launch_bwd_dkdv(d, true, tk, tv, tq, tdo, dk, dv, ws, B, H, max_seqlen, max_seqlen, all,
                                      info.num_sms, nullptr, s));
+}
+
+int sigattn_paged_reserve(const int32_t* cached_lens, const int32_t* new_lens, int32_t* block_table,
+                          const int32_t* free_pages, const int32_t* free_count, int32_t* free_count_out,
+                          int32_t* cu_seqlens, int32_t* kv_lens, int32_t* slots, int32_t* positions, int B,
+                          int max_pages, int page_size, int num_pages, int rows, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  DeviceInfo info;
+  int shift = 0;
+  const void* words[] = {cached_lens, new_lens, block_table, free_pages, free_count, free_count_out, cu_seqlens, kv_lens};
+  int st = check_pages(B, max_pages, page_size, num_pages, &shift);
+  if (st != SIGATTN_OK) return st;
+  for (const void* p : words)
+    if (!aligned4(p)) return SIGATTN_ERR_INVALID_ARG;
+  if (rows < 0 || (rows > 0 && !aligned4(slots)) || (positions != nullptr && !aligned4(positions)))
+    return SIGATTN_ERR_INVALID_ARG;
+  st = check_paged_call(workspace, workspace_bytes, kHeaderBytes, &info);
+  if (st != SIGATTN_OK) return st;
+  const PagedReserve a{cached_lens, new_lens, block_table, free_pages, free_count, free_count_out, cu_seqlens, kv_lens,
+                       slots, positions, B, max_pages, shift, num_pages, rows, static_cast<int*>(workspace)};
+  return cuda_status(launch_paged_reserve(a, info.num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int sigattn_paged_release(const int32_t* kv_lens, const int32_t* keep_lens, const int32_t* block_table,
+                          int32_t* free_pages, const int32_t* free_count, int32_t* free_count_out, int B,
+                          int max_pages, int page_size, int num_pages, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  DeviceInfo info;
+  int shift = 0;
+  int st = check_pages(B, max_pages, page_size, num_pages, &shift);
+  if (st != SIGATTN_OK) return st;
+  if (!aligned4(kv_lens) || (keep_lens != nullptr && !aligned4(keep_lens)) || !aligned4(block_table) ||
+      !aligned4(free_pages) || !aligned4(free_count) || !aligned4(free_count_out))
+    return SIGATTN_ERR_INVALID_ARG;
+  st = check_paged_call(workspace, workspace_bytes, kHeaderBytes, &info);
+  if (st != SIGATTN_OK) return st;
+  const PagedRelease a{kv_lens, keep_lens, block_table, free_pages, free_count, free_count_out, B, max_pages, shift,
+                       num_pages, static_cast<int*>(workspace)};
+  return cuda_status(launch_paged_release(a, info.num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int sigattn_paged_write(const void* k, long long k_stride, const void* v, long long v_stride, const int32_t* slots,
+                        void* k_cache, void* v_cache, const void* q, long long q_stride, void* q_out,
+                        long long q_out_stride, const int32_t* positions, const float* inv_freq,
+                        const int32_t* pair_axis, int axes, int pairs, int adjacent, int rows, int Hq, int Hkv, int d,
+                        int page_size, int num_pages, void* workspace, size_t workspace_bytes, void* stream) {
+  DeviceInfo info;
+  int shift = 0;
+  if (d != 64 && d != 128) return SIGATTN_ERR_UNSUPPORTED;
+  int st = check_pages(1, 1, page_size, num_pages, &shift);
+  if (st != SIGATTN_OK) return st;
+  const bool has_q = q != nullptr || q_out != nullptr;
+  if (rows < 0 || Hkv < 1 || (has_q && Hq < 1)) return SIGATTN_ERR_INVALID_ARG;
+  if (!cache_fits(num_pages, Hkv)) return SIGATTN_ERR_UNSUPPORTED;
+  if (Hkv > kMaxWriteHeads || (has_q && Hq > kMaxWriteHeads - 2 * Hkv)) return SIGATTN_ERR_UNSUPPORTED;
+  if (pairs < 0 || pairs % 8 != 0 || 2 * static_cast<long long>(pairs) > d) return SIGATTN_ERR_INVALID_ARG;
+  if (pairs > 0 && (axes < 1 || !aligned4(positions) || !aligned4(inv_freq) ||
+                    (pair_axis != nullptr && !aligned4(pair_axis))))
+    return SIGATTN_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return SIGATTN_ERR_INVALID_ARG;
+  if (rows > 0 && (!aligned16(k) || !aligned16(v) || !aligned4(slots) || !row_stride_ok(k_stride, Hkv, d) ||
+                   !row_stride_ok(v_stride, Hkv, d)))
+    return SIGATTN_ERR_INVALID_ARG;
+  if (has_q && rows > 0 && (!aligned16(q) || !aligned16(q_out) || !row_stride_ok(q_stride, Hq, d) ||
+                            !row_stride_ok(q_out_stride, Hq, d) || (q == q_out && q_stride != q_out_stride)))
+    return SIGATTN_ERR_INVALID_ARG;
+  st = check_paged_call(workspace, workspace_bytes, kHeaderBytes, &info);
+  if (st != SIGATTN_OK || rows == 0) return st;
+  using bf16 = __nv_bfloat16;
+  PagedWrite a{};
+  a.k = static_cast<const bf16*>(k);
+  a.v = static_cast<const bf16*>(v);
+  a.q = static_cast<const bf16*>(q);
+  a.k_cache = static_cast<bf16*>(k_cache);
+  a.v_cache = static_cast<bf16*>(v_cache);
+  a.q_out = static_cast<bf16*>(q_out);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_stride = q_stride;
+  a.q_out_stride = q_out_stride;
+  a.slots = slots;
+  a.positions = positions;
+  a.pair_axis = pair_axis;
+  a.inv_freq = inv_freq;
+  a.axes = axes;
+  a.pairs = pairs;
+  a.adjacent = adjacent != 0;
+  a.rows = rows;
+  a.Hq = has_q ? Hq : 0;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.page_shift = shift;
+  a.num_pages = num_pages;
+  a.ws = static_cast<int*>(workspace);
+  return cuda_status(launch_paged_write(a, info.num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sigattn_paged_workspace_size(int Hq, int Hkv, int d, int max_seqlen_q) {
+  if (check_paged_heads(Hq, Hkv, d) != SIGATTN_OK || max_seqlen_q < 1 || max_seqlen_q > kMaxPagedLen) return 0;
+  return kHeaderBytes;
+}
+
+int sigattn_fwd_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, void* o,
+                      const int32_t* cu_seqlens, const int32_t* kv_lens, const int32_t* block_table, int B, int Hq,
+                      int Hkv, int max_seqlen_q, int total, int max_pages, int page_size, int num_pages, int d,
+                      int causal, void* workspace, size_t workspace_bytes, void* stream) {
+  DeviceInfo info;
+  int shift = 0;
+  int st = check_paged_heads(Hq, Hkv, d);
+  if (st == SIGATTN_OK) st = check_pages(B, max_pages, page_size, num_pages, &shift);
+  if (st != SIGATTN_OK) return st;
+  if (max_seqlen_q < 1 || total < 0) return SIGATTN_ERR_INVALID_ARG;
+  if (max_seqlen_q > kMaxPagedLen || total > kMaxPackedTokens || !cache_fits(num_pages, Hkv))
+    return SIGATTN_ERR_UNSUPPORTED;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(cu_seqlens) || !aligned4(kv_lens) ||
+      !aligned4(block_table))
+    return SIGATTN_ERR_INVALID_ARG;
+  if (total > 0 && (!aligned16(q) || !aligned16(o) || !row_stride_ok(q_stride, Hq, d))) return SIGATTN_ERR_INVALID_ARG;
+  st = check_paged_call(workspace, workspace_bytes, sigattn_paged_workspace_size(Hq, Hkv, d, max_seqlen_q), &info);
+  if (st != SIGATTN_OK || total == 0) return st;
+  using bf16 = __nv_bfloat16;
+  const PagedAttend a{static_cast<const bf16*>(q), static_cast<const bf16*>(k_cache), static_cast<const bf16*>(v_cache),
+                      static_cast<bf16*>(o), q_stride, cu_seqlens, kv_lens, block_table, B, Hq, Hkv, max_seqlen_q, total,
+                      max_pages, shift, num_pages, d, causal != 0, static_cast<int*>(workspace)};
+  return cuda_status(launch_fwd_paged(a, info.num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 int sigattn_plan(const int32_t* lengths, int B, int H, int Lmax, int d, int kind, void* workspace,

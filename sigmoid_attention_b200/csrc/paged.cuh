@@ -1,0 +1,75 @@
+// paged.cuh -- arguments of the paged-cache kernels (pages.cu, paged.cu).
+#pragma once
+
+#include "common.cuh"
+
+namespace sigattn {
+
+constexpr int kMaxPagedLen = 1 << 24;  // tokens of one sequence (max_pages * page_size)
+constexpr int kMaxPagedGroup = 128;    // query heads per key/value head
+
+struct PagedReserve {
+  const int *cached, *fresh;  // [B]
+  int* table;                 // [B][max_pages]
+  const int* free_pages;
+  const int* free_count;
+  int* free_count_out;
+  int *cu, *kv, *slots, *positions;
+  int B, max_pages, page_shift, num_pages, rows;
+  int* ws;
+};
+
+struct PagedRelease {
+  const int *kv, *keep;  // [B]; keep may be null
+  const int* table;
+  int* free_pages;
+  const int* free_count;
+  int* free_count_out;
+  int B, max_pages, page_shift, num_pages;
+  int* ws;
+};
+
+// Cosine/sine entries of one buffer of the write kernel (tokens * pairs).
+constexpr int kWriteTurns = 512;
+
+struct PagedWrite {
+  const __nv_bfloat16 *k, *v, *q;
+  __nv_bfloat16 *k_cache, *v_cache, *q_out;
+  long long k_stride, v_stride, q_stride, q_out_stride;
+  const int *slots, *positions, *pair_axis;
+  const float* inv_freq;
+  int axes, pairs, adjacent, rows, Hq, Hkv, d, page_shift, num_pages;
+  int tokens;  // tokens a CTA takes at a time (set by the launcher)
+  int* ws;
+};
+
+struct PagedAttend {
+  const __nv_bfloat16 *q, *k_cache, *v_cache;
+  __nv_bfloat16* o;
+  long long q_stride;
+  const int *cu, *kv, *table;
+  int B, Hq, Hkv, max_q, total, max_pages, page_shift, num_pages, d, causal;
+  int* ws;
+};
+
+// One pair in one word (x1 low, x2 high) turned by (cos, sin) = cs.
+__device__ __forceinline__ uint32_t turn_word(uint32_t w, float2 cs) {
+  const float x1 = __uint_as_float(w << 16), x2 = __uint_as_float(w & 0xffff0000u);
+  return pack_bf16x2(x1 * cs.x - x2 * cs.y, x2 * cs.x + x1 * cs.y);
+}
+
+// Two pairs: first members in the halves of x, second members in those of y.
+__device__ __forceinline__ void turn_words(uint32_t& x, uint32_t& y, float2 lo, float2 hi) {
+  const float x1 = __uint_as_float(x << 16), x2 = __uint_as_float(y << 16);
+  const float z1 = __uint_as_float(x & 0xffff0000u), z2 = __uint_as_float(y & 0xffff0000u);
+  x = pack_bf16x2(x1 * lo.x - x2 * lo.y, z1 * hi.x - z2 * hi.y);
+  y = pack_bf16x2(x2 * lo.x + x1 * lo.y, z2 * hi.x + z1 * hi.y);
+}
+
+// Raise SIGATTN_ERR_INVALID_ARG with `site` in the workspace header.
+__device__ __forceinline__ void raise_invalid(int* ws, int site) {
+  atomicCAS(ws + kHdrError, 0, 1 /* SIGATTN_ERR_INVALID_ARG */);
+  atomicExch(ws + kHdrErrorSite, site);
+}
+
+}  // namespace sigattn

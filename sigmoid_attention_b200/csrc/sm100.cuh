@@ -25,6 +25,7 @@ enum : int {
   kHdrCount = 2,      // number of work items in the list
   kHdrNext = 3,       // work-item claim counter of the compute kernels (zeroed by the plan)
   kHdrFill = 4,       // zero-fill unit claim counter of the dQ kernel (zeroed by the plan)
+  kHdrTicket = 5,     // CTAs of a paged-cache call that have finished (back at zero after each call)
   kHeaderWords = 64,  // 256 bytes
 };
 
