@@ -40,6 +40,8 @@ cudaError_t launch_paged_reserve(const PagedReserve& a, int num_sms, cudaStream_
 cudaError_t launch_paged_release(const PagedRelease& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_paged_write(PagedWrite a, int num_sms, cudaStream_t stream);
 cudaError_t launch_fwd_paged(const PagedAttend& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_paged_few(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttend& a,
+                             int grid, cudaStream_t stream);
 void set_last_error(const char* msg);
 }  // namespace sigattn
 
@@ -130,6 +132,22 @@ bool make_map_packed(CUtensorMap* map, const void* ptr, int total, int H, int d,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3-D view {d, Hq, total} of rows of [Hq][d] bf16 with `stride` elements between
+// them, loaded as [tokens][heads][64 columns] boxes (a shared-memory image of
+// tokens * heads rows). Tokens past `total` read as zeros.
+bool make_map_rows(CUtensorMap* map, const void* ptr, int total, int Hq, long long stride, int d, int heads, int tokens) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(Hq),
+                              static_cast<cuuint64_t>(total)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens)};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, elem,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Packed token count bound: token coordinates start_b + row (row < n_b + 256)
 // stay in int32.
 constexpr int kMaxPackedTokens = INT_MAX - 4096;
@@ -194,6 +212,9 @@ int check_paged_heads(int Hq, int Hkv, int d) {
   if (Hq / Hkv > kMaxPagedGroup || Hq > (1 << 20)) return SIGATTN_ERR_UNSUPPORTED;
   return SIGATTN_OK;
 }
+
+// Whether a call's rows per key/value head are few enough for paged_few.cu.
+bool paged_is_few(int Hq, int Hkv, int max_q) { return static_cast<long long>(Hq / Hkv) * max_q <= kFewRows; }
 
 // The workspace and device checks of a paged call.
 int check_paged_call(const void* ws, size_t ws_bytes, size_t need, DeviceInfo* info) {
@@ -652,7 +673,8 @@ int sigattn_paged_write(const void* k, long long k_stride, const void* v, long l
 
 size_t sigattn_paged_workspace_size(int Hq, int Hkv, int d, int max_seqlen_q) {
   if (check_paged_heads(Hq, Hkv, d) != SIGATTN_OK || max_seqlen_q < 1 || max_seqlen_q > kMaxPagedLen) return 0;
-  return kHeaderBytes;
+  const size_t rows = paged_is_few(Hq, Hkv, max_seqlen_q) ? kFewRows : kFwdItemRows;
+  return kHeaderBytes + 2 * kMaxPagedCtas * rows * d * sizeof(float);
 }
 
 int sigattn_fwd_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, void* o,
@@ -674,10 +696,20 @@ int sigattn_fwd_paged(const void* q, long long q_stride, const void* k_cache, co
   st = check_paged_call(workspace, workspace_bytes, sigattn_paged_workspace_size(Hq, Hkv, d, max_seqlen_q), &info);
   if (st != SIGATTN_OK || total == 0) return st;
   using bf16 = __nv_bfloat16;
+  const int G = Hq / Hkv;
   const PagedAttend a{static_cast<const bf16*>(q), static_cast<const bf16*>(k_cache), static_cast<const bf16*>(v_cache),
                       static_cast<bf16*>(o), q_stride, cu_seqlens, kv_lens, block_table, B, Hq, Hkv, max_seqlen_q, total,
-                      max_pages, shift, num_pages, d, causal != 0, static_cast<int*>(workspace)};
-  return cuda_status(launch_fwd_paged(a, info.num_sms, static_cast<cudaStream_t>(stream)));
+                      max_pages, shift, num_pages, d, causal != 0, 1,
+                      reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes),
+                      static_cast<int*>(workspace)};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!paged_is_few(Hq, Hkv, max_seqlen_q)) return cuda_status(launch_fwd_paged(a, info.num_sms, s));
+  CUtensorMap tq, tk, tv;
+  if (!make_map_rows(&tq, q, total, Hq, q_stride, d, G, max_seqlen_q) ||
+      !make_map(&tk, k_cache, num_pages * Hkv, page_size, d, std::min(page_size, 128)) ||
+      !make_map(&tv, v_cache, num_pages * Hkv, page_size, d, std::min(page_size, 128)))
+    return map_failure();
+  return cuda_status(launch_paged_few(tq, tk, tv, a, std::min(info.num_sms, kMaxPagedCtas), s));
 }
 
 int sigattn_plan(const int32_t* lengths, int B, int H, int Lmax, int d, int kind, void* workspace,
@@ -733,7 +765,9 @@ int sigattn_read_error(void* workspace, int* site, void* stream) {
   int hdr[2] = {0, 0};
   cudaError_t e = cudaMemcpyAsync(hdr, workspace, sizeof(hdr), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(workspace, 0, sizeof(hdr), s);
+  // An expired wait may leave counts behind in the header: clear all of it.
+  const size_t clear = hdr[kHdrError] == SIGATTN_ERR_TIMEOUT ? kHeaderBytes : sizeof(hdr);
+  if (e == cudaSuccess) e = cudaMemsetAsync(workspace, 0, clear, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_status(e);
   if (site) *site = hdr[kHdrErrorSite];

@@ -49,8 +49,15 @@ struct PagedAttend {
   long long q_stride;
   const int *cu, *kv, *table;
   int B, Hq, Hkv, max_q, total, max_pages, page_shift, num_pages, d, causal;
+  int least;     // fewest units of work in a CTA's run
+  float* parts;  // partial sums of tiles cut over CTAs, two places per CTA
   int* ws;
 };
+
+// CTAs of a paged attention call at most (the workspace holds two parts each).
+constexpr int kMaxPagedCtas = 152;
+// Query rows per key/value head (G * new tokens) up to which paged_few.cu serves.
+constexpr int kFewRows = 64;
 
 // One pair in one word (x1 low, x2 high) turned by (cos, sin) = cs.
 __device__ __forceinline__ uint32_t turn_word(uint32_t w, float2 cs) {

@@ -1,0 +1,466 @@
+// paged_few.cu -- sigmoid attention of a few new tokens per sequence over a
+// paged cache (at most 64 query rows per key/value head: G query heads times
+// the new tokens).
+//
+//   o_i = sum_{j < N} sigma(q_i . k_j / sqrt(d) - ln N) v_j
+//
+// So few rows leave the work bound by reading K and V once. What that needs:
+// every SM reads all the time, whatever the lengths are, and the arithmetic
+// on a block keeps out of the way of the reads.
+//
+//  * Split. The unit of work is a block of 128 keys of one (sequence, key/value
+//    head). All units of the call stand in one line (sequences, heads,
+//    blocks), which is cut into equal runs, one per CTA: a run ends inside
+//    a text where the cut falls, so ragged batches and single long texts
+//    load the SMs alike. Weights of a sigmoid carry no row maximum or sum, so the
+//    parts of a text cut over CTAs just add up: each stores fp32 partial
+//    sums, and the CTA that stores last adds them in CTA order (fixed, so a
+//    repeated call gives the same bits) and rounds once.
+//  * The CTAs find their runs themselves, with one prefix sum over the batch's
+//    lengths; there is no plan launch.
+//  * Orientation. The keys are the 128 rows of the products, the queries the
+//    columns: S^T = K Q^T (128 x NR) and O^T += V^T P^T (D x NR), NR = 16, 32 or
+//    64. A product's time follows its columns, so a block costs an eighth to a
+//    half of what it would with the queries padded to 128 rows, and each
+//    epilogue thread owns one key: its NR weights go to shared memory as one
+//    row of the second product's B operand.
+//
+// Roles (11 warps): 0-7 epilogue in two groups of four that take blocks in
+// turn (thread = key), 8 the producer (plan, page tables, TMA), 9 the issuer of
+// S^T, 10 the issuer of O^T.
+#include "paged_run.cuh"
+
+namespace sigattn {
+
+namespace {
+
+template <int D, int NR>
+struct FewCfg {
+  static constexpr int CH = D / 64;                     // 64-column chunks of a row
+  static constexpr int BOX_BYTES = kKeyBlock * 128;    // [128 keys][64 columns]
+  static constexpr int TILE_BYTES = CH * BOX_BYTES;
+  // About 150 KB of K and V tiles are on the way or in use. K and V have rings
+  // of their own: a slot is then awaited by one role only, which sees each
+  // of its phases (a role that skipped one could take an earlier phase of the
+  // same parity for the one it waits for). V tiles stay longer: they wait for P.
+  static constexpr int KST = D == 64 ? 4 : 2;
+  static constexpr int VST = D == 64 ? 5 : (NR == 64 ? 2 : 3);
+  static constexpr int STAGES = KST + VST;
+  static constexpr int Q_CHUNK = NR * 128;
+  static constexpr int Q_BYTES = CH * Q_CHUNK;
+  static constexpr int P_BYTES = kKeyBlock * 128;      // rows of 64 columns, NR of them in use
+  static constexpr int OFF_P = STAGES * TILE_BYTES;
+  static constexpr int OFF_Q = OFF_P + 2 * P_BYTES;
+  static constexpr int SMEM_ALLOC = OFF_Q + 2 * Q_BYTES + 1024;
+  static_assert(SMEM_ALLOC <= 220 * 1024, "shared memory budget");
+  static constexpr int TM_S = 0;                        // two S^T regions, then two O^T regions
+  static constexpr int TM_O = 2 * NR;
+  static constexpr int TMEM_COLS = 4 * NR;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int WARPS = EPI_WARPS + 3;
+  static constexpr int THREADS = WARPS * 32;
+};
+
+template <int STAGES>
+struct FewBarriers {
+  uint64_t full[STAGES], empty[STAGES];  // K slots first, then V slots
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], s_empty[2];
+  uint64_t p_full[2], p_empty[2];
+  uint64_t o_full[2], o_empty[2];
+  uint64_t stored, counted, drain[2];
+  SegRing ring;
+  PlanRun run;
+  uint32_t tmem_base;
+  int abort, last;
+};
+
+}  // namespace
+
+template <int D, int NR>
+__global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
+    paged_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const PagedAttend a) {
+  using C = FewCfg<D, NR>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ FewBarriers<C::STAGES> bar;
+  __shared__ float s_log2n[C::EPI_WARPS][NR];  // each epilogue warp's log2 N and N of the segment's rows
+  __shared__ int s_seen[C::EPI_WARPS][NR];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sP = smem + C::OFF_P;
+  uint8_t* sQ = smem + C::OFF_Q;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &bar.abort;
+  int* ws = a.ws;
+  constexpr int kProducer = C::EPI_WARPS, kIssueS = kProducer + 1, kIssueO = kProducer + 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&bar.full[s], 1);
+      mbar_init(&bar.empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar.q_full[s], 1);
+      mbar_init(&bar.q_empty[s], 1);
+      mbar_init(&bar.s_full[s], 1);
+      mbar_init(&bar.s_empty[s], 4);
+      mbar_init(&bar.p_full[s], 4);
+      mbar_init(&bar.p_empty[s], 1);
+      mbar_init(&bar.o_full[s], 1);
+      mbar_init(&bar.o_empty[s], C::EPI_WARPS);
+      mbar_init(&bar.drain[s], 1);
+    }
+    mbar_init(&bar.stored, C::EPI_WARPS);
+    mbar_init(&bar.counted, 1);
+    seg_ring_init(bar.ring, C::EPI_WARPS + 2);
+    bar.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kIssueO) {
+    tmem_alloc(&bar.tmem_base, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  // Query rows that no load covers stay zero.
+  for (int i = threadIdx.x; i < 2 * C::Q_BYTES / 16; i += C::THREADS)
+    reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  grid_dep_launch();
+  grid_dep_wait();
+  plan_run<C::THREADS>(a, &bar.run, [](const SeqInfo& s) { return seq_blocks(s.n); });
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem_base;
+  const int G = a.Hq / a.Hkv;
+
+  if (warp == kProducer) {
+    // ------------------------------------------------------------- producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    const int rb = min(1 << a.page_shift, kKeyBlock);  // keys per box
+    const int q_bytes = min(a.max_q * G, NR) * 128 * C::CH;
+    uint32_t qb = 0, qph = 0, rst = 0, rph = 0;
+    uint32_t loads[2] = {0, 0}, q_used = 0;  // K, V and Q tiles loaded, for an aborting producer
+    uint32_t st[2] = {0, 0}, ph[2] = {0, 0};
+    bool ok = true;
+    // The run, one segment at a time.
+    const PlanRun run = bar.run;
+    long long unit = run.first, left = run.count;
+    Segment seg{};
+    int blocks = 1;
+    if (left > 0) {
+      SeqInfo s;
+      seq_info(a, run.b, &s);
+      blocks = seq_blocks(s.n);
+      seg = Segment{s.start, s.m, s.n, run.b, static_cast<int>(run.rem / blocks), 0, static_cast<int>(run.rem % blocks),
+                    0, blocks, 0, 0, 0};
+    }
+    while (ok && left > 0) {
+      const int len = static_cast<int>(min(left, static_cast<long long>(blocks - seg.j0)));
+      seg.j1 = seg.j0 + len;
+      seg.first_cta = static_cast<int>((unit - seg.j0) / run.per);
+      seg.last_cta = static_cast<int>((unit - seg.j0 + blocks - 1) / run.per);
+      if (!(ok = seg_publish(bar.ring, rst, rph, seg, lane, abort_flag, ws, 300))) break;
+      PageWindow pages(a, seg.b, seg.n, seg.j0 * kKeyBlock, lane);
+      if (!(ok = warp_wait(&bar.q_empty[qb], qph ^ 1, abort_flag, ws, 301))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bar.q_full[qb], q_bytes);
+        for (int c = 0; c < C::CH; ++c)
+          tma_load_3d(sQ + qb * C::Q_BYTES + c * C::Q_CHUNK, &tm_q, &bar.q_full[qb], c * 64, seg.head * G, seg.start);
+      }
+      ++q_used;
+      if ((qb ^= 1) == 0) qph ^= 1;
+      for (int j = seg.j0; ok && j < seg.j1; ++j) {
+        const int keys = min(kKeyBlock, seg.n - j * kKeyBlock);
+        const int boxes = (keys + rb - 1) / rb;  // 0 for a sequence without keys
+        int row;
+        const int z = pages.locate(a, j * kKeyBlock, lane / C::CH, rb, lane / C::CH < boxes, seg.head, &row);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t slot = (kv ? C::KST : 0) + st[kv];
+          if (!(ok = warp_wait(&bar.empty[slot], ph[kv] ^ 1, abort_flag, ws, 302))) break;
+          if (lane == 0) mbar_arrive_expect_tx(&bar.full[slot], boxes * rb * 128 * C::CH);
+          __syncwarp();
+          if (lane < boxes * C::CH)
+            tma_load_3d(smem + slot * C::TILE_BYTES + (lane % C::CH) * C::BOX_BYTES + (lane / C::CH) * rb * 128,
+                        kv ? &tm_v : &tm_k, &bar.full[slot], (lane % C::CH) * 64, row, z);
+          __syncwarp();
+          ++loads[kv];
+          if (++st[kv] == (kv ? C::VST : C::KST)) { st[kv] = 0; ph[kv] ^= 1; }
+        }
+      }
+      unit += len;
+      left -= len;
+      seg.j0 = 0;
+      if (left > 0 && ++seg.head == a.Hkv) {  // on to the next sequence with new tokens
+        seg.head = 0;
+        SeqInfo s;
+        do seq_info(a, ++seg.b, &s); while (s.m == 0 && seg.b + 1 < a.B);
+        if (s.m == 0) break;
+        seg.start = s.start;
+        seg.m = s.m;
+        seg.n = s.n;
+        seg.blocks = blocks = seq_blocks(s.n);
+      }
+    }
+    if (ok) {
+      seg.j1 = -1;
+      ok = seg_publish(bar.ring, rst, rph, seg, lane, abort_flag, ws, 303);
+    }
+    if (!ok) {  // aborting: let the copies in flight land before the CTA exits
+      int never = 0;
+      volatile int* no_abort = &never;
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t slots = kv ? C::VST : C::KST;
+        for (uint32_t s = 0; s < slots && s < loads[kv]; ++s) {
+          const uint32_t idx = loads[kv] - 1 - s;
+          mbar_wait(&bar.full[(kv ? C::KST : 0) + idx % slots], (idx / slots) & 1, no_abort, nullptr, 0);
+        }
+      }
+      for (uint32_t s = 0; s < 2 && s < q_used; ++s)
+        mbar_wait(&bar.q_full[(q_used - 1 - s) & 1], ((q_used - 1 - s) >> 1) & 1, no_abort, nullptr, 0);
+    }
+  } else if (warp == kIssueS) {
+    // ------------------------------------------------- S^T = K Q^T (128 x NR)
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, NR, false, false);
+      const uint64_t d_k = smem_desc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t d_q = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      uint32_t st = 0, ph = 0, qb = 0, qph = 0, sb = 0, sph = 0, rst = 0, rph = 0;
+      bool ok = true;
+      while (ok) {
+        Segment seg;
+        if (!(ok = seg_read<false>(bar.ring, rst, rph, &seg, abort_flag, ws, 310))) break;
+        seg_release(bar.ring, rst, rph, true);
+        if (seg.j1 < 0) break;
+        if (!(ok = mbar_wait(&bar.q_full[qb], qph, abort_flag, ws, 311))) break;
+        for (int j = seg.j0; j < seg.j1; ++j) {
+          if (!(ok = mbar_wait(&bar.full[st], ph, abort_flag, ws, 312))) break;
+          if (!(ok = mbar_wait(&bar.s_empty[sb], sph ^ 1, abort_flag, ws, 313))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + C::TM_S + sb * NR, d_k + ((st * C::TILE_BYTES + (kk >> 2) * C::BOX_BYTES + (kk & 3) * 32) >> 4),
+                   d_q + ((qb * C::Q_BYTES + (kk >> 2) * C::Q_CHUNK + (kk & 3) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
+          mma_commit(&bar.s_full[sb]);
+          mma_commit(&bar.empty[st]);
+          if (j + 1 == seg.j1) mma_commit(&bar.q_empty[qb]);
+          if ((sb ^= 1) == 0) sph ^= 1;
+          if (++st == C::KST) { st = 0; ph ^= 1; }
+        }
+        if ((qb ^= 1) == 0) qph ^= 1;
+      }
+      int never = 0;
+      mma_commit(&bar.drain[0]);
+      mbar_wait(&bar.drain[0], 0, &never, ws, 319);
+    }
+  } else if (warp == kIssueO) {
+    // ------------------------------------------- O^T += V^T P^T (D x NR)
+    // At D = 64 the product's 128 rows hold V's 64 columns twice (the second
+    // column block's distance is 0); the second half is not read.
+    constexpr uint32_t idesc = idesc_bf16_f32(128, NR, true, true);
+    const uint64_t d_v = smem_desc_sw128(smem_u32(smem), D == 64 ? 0 : C::BOX_BYTES, 1024);
+    const uint64_t d_p = smem_desc_sw128(smem_u32(sP), C::P_BYTES, 1024);
+    uint32_t st = C::KST, ph = 0, pb = 0, pph = 0, ob = 0, oph = 0, rst = 0, rph = 0;
+    bool ok = true;
+    while (ok) {
+      Segment seg;
+      if (!(ok = seg_read<true>(bar.ring, rst, rph, &seg, abort_flag, ws, 320))) break;
+      __syncwarp();
+      seg_release(bar.ring, rst, rph, lane == 0);
+      if (seg.j1 < 0) break;
+      for (int j = seg.j0; j < seg.j1; ++j) {
+        if (!(ok = warp_wait(&bar.full[st], ph, abort_flag, ws, 321))) break;
+        // The product takes keys in sixteens. Rows of V past the text's end in
+        // the last sixteen hold whatever the page (or an earlier tile) held;
+        // their weights are 0, and 0 * NaN must not be: they are zeroed.
+        const int keys = min(kKeyBlock, seg.n - j * kKeyBlock);
+        const int steps = max(1, (keys + 15) / 16);
+        if (keys < steps * 16) {
+          uint4* v = reinterpret_cast<uint4*>(smem + st * C::TILE_BYTES);
+          for (int i = lane; i < (steps * 16 - keys) * 8; i += 32)
+            for (int c = 0; c < C::CH; ++c) v[(c * C::BOX_BYTES + keys * 128) / 16 + i] = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (!(ok = warp_wait(&bar.p_full[pb], pph, abort_flag, ws, 322))) break;
+        if (j == seg.j0 && !(ok = warp_wait(&bar.o_empty[ob], oph ^ 1, abort_flag, ws, 323))) break;
+        tc_fence_after();
+        if (lane == 0) {
+          for (int kk = 0; kk < steps; ++kk)
+            mma_ss(tmem + C::TM_O + ob * NR, d_v + ((st * C::TILE_BYTES + kk * 2048) >> 4),
+                   d_p + ((pb * C::P_BYTES + kk * 2048) >> 4), idesc, (j > seg.j0 || kk > 0) ? 1u : 0u);
+          mma_commit(&bar.empty[st]);
+          mma_commit(&bar.p_empty[pb]);
+          if (j + 1 == seg.j1) mma_commit(&bar.o_full[ob]);
+        }
+        __syncwarp();
+        if ((pb ^= 1) == 0) pph ^= 1;
+        if (++st == C::STAGES) { st = C::KST; ph ^= 1; }
+      }
+      if ((ob ^= 1) == 0) oph ^= 1;
+    }
+    if (lane == 0) {
+      int never = 0;
+      mma_commit(&bar.drain[1]);
+      mbar_wait(&bar.drain[1], 0, &never, ws, 329);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- epilogue
+    const int g = warp >> 2;                       // this group's blocks, S region and P buffer
+    const int quad = warp & 3;
+    const int key = (quad << 5) + lane;            // key within the block = TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>(quad << 5) << 16;
+    constexpr float scale_l2e = Scale<D>::value * kLog2e;
+    uint8_t* prow = sP + g * C::P_BYTES + key * 128;
+    uint32_t t = 0, sph = 0, pph = 0, ob = 0, oph = 0, rst = 0, rph = 0, parts = 0;
+    float* my_log2n = s_log2n[warp];
+    int* my_seen = s_seen[warp];
+    bool ok = true;
+    while (ok) {
+      Segment seg;
+      if (!(ok = seg_read<true>(bar.ring, rst, rph, &seg, abort_flag, ws, 330))) break;
+      __syncwarp();
+      seg_release(bar.ring, rst, rph, lane == 0);
+      if (seg.j1 < 0) break;
+      // N and log2 N of each row (column of S^T); rows past the last see nothing.
+      const int rows = seg.m * G;
+      int least = seg.n;
+      for (int n = lane; n < NR; n += 32) {
+        int seen = seg.n;
+        if (a.causal) seen = max(0, min(seg.n, seg.n - seg.m + n / G + 1));
+        my_seen[n] = n < rows ? seen : 0;
+        my_log2n[n] = log2f(static_cast<float>(max(seen, 1)));
+      }
+      if (a.causal) least = max(0, seg.n - seg.m + 1);
+      __syncwarp();
+      for (int j = seg.j0; j < seg.j1; ++j, ++t) {
+        if ((t & 1) != static_cast<uint32_t>(g)) continue;
+        if (!(ok = warp_wait(&bar.s_full[g], sph, abort_flag, ws, 331))) break;
+        tc_fence_after();
+        uint32_t s[NR];
+        if constexpr (NR == 16) {
+          tmem_ld16(tmem + lane_off + C::TM_S + g * NR, s);
+        } else {
+#pragma unroll
+          for (int c = 0; c < NR / 32; ++c)
+            tmem_ld32(tmem + lane_off + C::TM_S + g * NR + 32 * c, reinterpret_cast<uint32_t(&)[32]>(s[32 * c]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.s_empty[g]);
+        if ((j + 1) * kKeyBlock > least) {
+          const int at = j * kKeyBlock + key;
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+            if (at >= my_seen[n]) s[n] = 0xff800000u;  // -inf: weight 0
+        }
+        // sigma(x) = 1 / (1 + 2^(log2 N - s scale log2 e)). Two MUFU operations
+        // per weight, which this kernel's few weights allow: both are exact to
+        // about 1e-7, where the polynomial of the whole-sequence kernels
+        // (sigmoid_n) spends 9e-4.
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+          s[n] = __float_as_uint(rcp_approx(
+              1.0f + ex2_approx(fmaf(__uint_as_float(s[n]), -scale_l2e, my_log2n[n]))));
+        if (!(ok = warp_wait(&bar.p_empty[g], pph ^ 1, abort_flag, ws, 332))) break;
+#pragma unroll
+        for (int c = 0; c < NR / 8; ++c) {
+          const uint32_t* w = s + 8 * c;
+          *reinterpret_cast<uint4*>(prow + ((c ^ (key & 7)) << 4)) =
+              make_uint4(pack_bf16x2(__uint_as_float(w[0]), __uint_as_float(w[1])),
+                         pack_bf16x2(__uint_as_float(w[2]), __uint_as_float(w[3])),
+                         pack_bf16x2(__uint_as_float(w[4]), __uint_as_float(w[5])),
+                         pack_bf16x2(__uint_as_float(w[6]), __uint_as_float(w[7])));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[g]);
+        sph ^= 1;
+        pph ^= 1;
+      }
+      if (!ok) break;
+      // O^T: thread = column d of the output, the group's half of the rows.
+      if (!(ok = warp_wait(&bar.o_full[ob], oph, abort_flag, ws, 333))) break;
+      tc_fence_after();
+      constexpr int HR = NR / 2;
+      uint32_t o[HR];
+      tmem_ld_cols(tmem + lane_off + C::TM_O + ob * NR + g * HR, o);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.o_empty[ob]);
+      if ((ob ^= 1) == 0) oph ^= 1;
+      const int n0 = g * HR, dcol = key;
+      const bool mine = D == 128 || dcol < D;
+      auto out_at = [&](int n) {
+        return a.o + (static_cast<size_t>(seg.start + n / G) * a.Hq + seg.head * G + n % G) * D + dcol;
+      };
+      if (seg.j0 == 0 && seg.j1 == seg.blocks) {
+#pragma unroll
+        for (int i = 0; i < HR; ++i)
+          if (mine && n0 + i < rows) *out_at(n0 + i) = __float2bfloat16(__uint_as_float(o[i]));
+        continue;
+      }
+      float* part = a.parts + static_cast<size_t>(2 * blockIdx.x + (seg.j0 == 0)) * (NR * D);
+#pragma unroll
+      for (int i = 0; i < HR; ++i)
+        if (mine && n0 + i < rows) __stcg(part + (n0 + i) * D + dcol, __uint_as_float(o[i]));
+      if (!(ok = last_part(&bar.stored, &bar.counted, &bar.last, seg, ws, warp, lane, parts, abort_flag, 334))) break;
+      parts ^= 1;
+      if (bar.last) {
+        const int np = seg.last_cta - seg.first_cta + 1;
+        const float* from = a.parts + static_cast<size_t>(2 * seg.first_cta) * (NR * D) + dcol;
+        for (int i = 0; i < HR && n0 + i < rows; ++i) {
+          if (!mine) break;
+          // the first part lies in its CTA's second place, the others in their CTA's first
+          float sum = __ldcg(from + NR * D + (n0 + i) * D);
+#pragma unroll 8
+          for (int p = 1; p < np; ++p) sum += __ldcg(from + static_cast<size_t>(2 * p) * (NR * D) + (n0 + i) * D);
+          *out_at(n0 + i) = __float2bfloat16(sum);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssueO) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+namespace {
+
+template <int D, int NR>
+cudaError_t launch_few_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttend& a,
+                            int grid, cudaStream_t stream) {
+  using C = FewCfg<D, NR>;
+  static PerDeviceOnce attr;
+  const cudaError_t e = attr.run([] {
+    return cudaFuncSetAttribute(paged_few_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_programmatic(paged_few_kernel<D, NR>, dim3(grid), dim3(C::THREADS), C::SMEM_ALLOC, stream, tq, tk, tv, a);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_few(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttend& a,
+                             int grid, cudaStream_t stream) {
+  const int rows = a.max_q * (a.Hq / a.Hkv);
+  if (a.d == 64) {
+    if (rows <= 16) return launch_few_impl<64, 16>(tq, tk, tv, a, grid, stream);
+    if (rows <= 32) return launch_few_impl<64, 32>(tq, tk, tv, a, grid, stream);
+    return launch_few_impl<64, 64>(tq, tk, tv, a, grid, stream);
+  }
+  if (rows <= 16) return launch_few_impl<128, 16>(tq, tk, tv, a, grid, stream);
+  if (rows <= 32) return launch_few_impl<128, 32>(tq, tk, tv, a, grid, stream);
+  return launch_few_impl<128, 64>(tq, tk, tv, a, grid, stream);
+}
+
+}  // namespace sigattn
