@@ -16,7 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsigattn.so")
-SOURCES = ["api.cu", "plan.cu", "fwd.cu", "bwd.cu", "noalloc.cu", "pages.cu", "paged.cu", "paged_few.cu"]
+SOURCES = ["api.cu", "plan.cu", "fwd.cu", "bwd.cu", "noalloc.cu", "pages.cu", "paged_few.cu", "paged_many.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", os.path.join(ROOT, "include")]

@@ -39,7 +39,8 @@ cudaError_t launch_bwd_dkdv(int d, bool packed, const CUtensorMap& tk, const CUt
 cudaError_t launch_paged_reserve(const PagedReserve& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_paged_release(const PagedRelease& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_paged_write(PagedWrite a, int num_sms, cudaStream_t stream);
-cudaError_t launch_fwd_paged(const PagedAttend& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_paged_many(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttend& a,
+                              int grid, cudaStream_t stream);
 cudaError_t launch_paged_few(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttend& a,
                              int grid, cudaStream_t stream);
 void set_last_error(const char* msg);
@@ -703,13 +704,14 @@ int sigattn_fwd_paged(const void* q, long long q_stride, const void* k_cache, co
                       reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes),
                       static_cast<int*>(workspace)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (!paged_is_few(Hq, Hkv, max_seqlen_q)) return cuda_status(launch_fwd_paged(a, info.num_sms, s));
+  const bool few = paged_is_few(Hq, Hkv, max_seqlen_q);
   CUtensorMap tq, tk, tv;
-  if (!make_map_rows(&tq, q, total, Hq, q_stride, d, G, max_seqlen_q) ||
+  if (!make_map_rows(&tq, q, total, Hq, q_stride, d, G, few ? max_seqlen_q : 128 / G) ||
       !make_map(&tk, k_cache, num_pages * Hkv, page_size, d, std::min(page_size, 128)) ||
       !make_map(&tv, v_cache, num_pages * Hkv, page_size, d, std::min(page_size, 128)))
     return map_failure();
-  return cuda_status(launch_paged_few(tq, tk, tv, a, std::min(info.num_sms, kMaxPagedCtas), s));
+  const int grid = std::min(info.num_sms, kMaxPagedCtas);
+  return cuda_status(few ? launch_paged_few(tq, tk, tv, a, grid, s) : launch_paged_many(tq, tk, tv, a, grid, s));
 }
 
 int sigattn_plan(const int32_t* lengths, int B, int H, int Lmax, int d, int kind, void* workspace,

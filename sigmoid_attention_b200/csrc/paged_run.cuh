@@ -110,7 +110,8 @@ __device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun* run, Uni
 struct Segment {
   int start, m, n, b;
   int head, tile, j0, j1;
-  int blocks, first_cta, last_cta, unused;
+  int blocks, first_cta, last_cta;
+  int lead;  // the first CTA's units before the tile (a part p CTAs on starts at block p * per - lead)
 };
 static_assert(sizeof(Segment) == 48, "three int4");
 
@@ -134,7 +135,7 @@ __device__ __forceinline__ bool seg_publish(SegRing& r, uint32_t& st, uint32_t& 
   if (lane == 0) {
     r.slot[st][0] = make_int4(s.start, s.m, s.n, s.b);
     r.slot[st][1] = make_int4(s.head, s.tile, s.j0, s.j1);
-    r.slot[st][2] = make_int4(s.blocks, s.first_cta, s.last_cta, 0);
+    r.slot[st][2] = make_int4(s.blocks, s.first_cta, s.last_cta, s.lead);
     mbar_arrive(&r.full[st]);
   }
   __syncwarp();
@@ -142,14 +143,19 @@ __device__ __forceinline__ bool seg_publish(SegRing& r, uint32_t& st, uint32_t& 
   return true;
 }
 
-// WARP: a whole warp calls this (otherwise one thread of it).
+__device__ __forceinline__ Segment seg_peek(SegRing& r, uint32_t st) {
+  const int4 x = r.slot[st][0], y = r.slot[st][1], z = r.slot[st][2];
+  return Segment{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+}
+
+// Wait for the next segment and copy it out; its slot stays taken until
+// seg_release. WARP: a whole warp calls this (otherwise one thread of it).
 template <bool WARP>
 __device__ __forceinline__ bool seg_read(SegRing& r, uint32_t st, uint32_t ph, Segment* s, volatile int* abort_flag,
                                          int* ws, int site) {
   if (!(WARP ? warp_wait(&r.full[st], ph, abort_flag, ws, site) : mbar_wait(&r.full[st], ph, abort_flag, ws, site)))
     return false;
-  const int4 x = r.slot[st][0], y = r.slot[st][1], z = r.slot[st][2];
-  *s = Segment{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, 0};
+  *s = seg_peek(r, st);
   return true;
 }
 
