@@ -61,6 +61,15 @@ struct FewCfg {
   static constexpr int THREADS = WARPS * 32;
 };
 
+// All new tokens of a sequence make one tile.
+struct OneTile {
+  __device__ __forceinline__ int items(const SeqInfo&) const { return 1; }
+  __device__ __forceinline__ int blocks(const SeqInfo& s, int) const { return seq_blocks(s.n); }
+  __device__ __forceinline__ long long before(const SeqInfo& s, int k) const {
+    return static_cast<long long>(k) * seq_blocks(s.n);
+  }
+};
+
 template <int STAGES>
 struct FewBarriers {
   uint64_t full[STAGES], empty[STAGES];  // K slots first, then V slots
@@ -68,7 +77,7 @@ struct FewBarriers {
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full[2], p_empty[2];
   uint64_t o_full[2], o_empty[2];
-  uint64_t stored, counted, drain[2];
+  uint64_t stored, counted, joined, drain[2];
   SegRing ring;
   PlanRun run;
   uint32_t tmem_base;
@@ -112,6 +121,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     }
     mbar_init(&bar.stored, C::EPI_WARPS);
     mbar_init(&bar.counted, 1);
+    mbar_init(&bar.joined, C::EPI_WARPS);
     seg_ring_init(bar.ring, C::EPI_WARPS + 2);
     bar.abort = 0;
     fence_mbar_init();
@@ -146,25 +156,11 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     uint32_t loads[2] = {0, 0}, q_used = 0;  // K, V and Q tiles loaded, for an aborting producer
     uint32_t st[2] = {0, 0}, ph[2] = {0, 0};
     bool ok = true;
-    // The run, one segment at a time.
-    const PlanRun run = bar.run;
-    long long unit = run.first, left = run.count;
-    Segment seg{};
-    int blocks = 1;
-    if (left > 0) {
-      SeqInfo s;
-      seq_info(a, run.b, &s);
-      blocks = seq_blocks(s.n);
-      seg = Segment{s.start, s.m, s.n, run.b, static_cast<int>(run.rem / blocks), 0, static_cast<int>(run.rem % blocks),
-                    0, blocks, 0, 0, 0};
-    }
-    while (ok && left > 0) {
-      const int len = static_cast<int>(min(left, static_cast<long long>(blocks - seg.j0)));
-      seg.j1 = seg.j0 + len;
-      seg.first_cta = static_cast<int>((unit - seg.j0) / run.per);
-      seg.last_cta = static_cast<int>((unit - seg.j0 + blocks - 1) / run.per);
+    const OneTile tiles{};
+    RunWalker<OneTile> walk(a, tiles, bar.run, lane);
+    const Segment& seg = walk.seg;
+    for (bool more = bar.run.count > 0; ok && more; more = ok && walk.next()) {
       if (!(ok = seg_publish(bar.ring, rst, rph, seg, lane, abort_flag, ws, 300))) break;
-      PageWindow pages(a, seg.b, seg.n, seg.j0 * kKeyBlock, lane);
       if (!(ok = warp_wait(&bar.q_empty[qb], qph ^ 1, abort_flag, ws, 301))) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(&bar.q_full[qb], q_bytes);
@@ -177,7 +173,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
         const int keys = min(kKeyBlock, seg.n - j * kKeyBlock);
         const int boxes = (keys + rb - 1) / rb;  // 0 for a sequence without keys
         int row;
-        const int z = pages.locate(a, j * kKeyBlock, lane / C::CH, rb, lane / C::CH < boxes, seg.head, &row);
+        const int z = walk.locate(j, lane / C::CH, rb, lane / C::CH < boxes, &row);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           const uint32_t slot = (kv ? C::KST : 0) + st[kv];
@@ -192,24 +188,8 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
           if (++st[kv] == (kv ? C::VST : C::KST)) { st[kv] = 0; ph[kv] ^= 1; }
         }
       }
-      unit += len;
-      left -= len;
-      seg.j0 = 0;
-      if (left > 0 && ++seg.head == a.Hkv) {  // on to the next sequence with new tokens
-        seg.head = 0;
-        SeqInfo s;
-        do seq_info(a, ++seg.b, &s); while (s.m == 0 && seg.b + 1 < a.B);
-        if (s.m == 0) break;
-        seg.start = s.start;
-        seg.m = s.m;
-        seg.n = s.n;
-        seg.blocks = blocks = seq_blocks(s.n);
-      }
     }
-    if (ok) {
-      seg.j1 = -1;
-      ok = seg_publish(bar.ring, rst, rph, seg, lane, abort_flag, ws, 303);
-    }
+    if (ok) ok = seg_publish(bar.ring, rst, rph, end_segment(), lane, abort_flag, ws, 303);
     if (!ok) {  // aborting: let the copies in flight land before the CTA exits
       int never = 0;
       volatile int* no_abort = &never;
@@ -318,6 +298,72 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     constexpr float scale_l2e = Scale<D>::value * kLog2e;
     uint8_t* prow = sP + g * C::P_BYTES + key * 128;
     uint32_t t = 0, sph = 0, pph = 0, ob = 0, oph = 0, rst = 0, rph = 0, parts = 0;
+    // The sum of a tile's parts, by all epilogue warps: `rows` rows of D, four at
+    // a time. Lanes take four columns each, so a warp reads SUB rows of a part
+    // at once; part p belongs to slice p % SLICES, the slices are added in order.
+    // The P buffers hold the slices' sums: every product that reads them has
+    // completed, and the next weights are written after the last barrier below.
+    uint32_t red_ph = 0;
+    auto join = [&](const Segment& seg, int rows) -> bool {
+      constexpr int LPR = D / 4, SUB = 32 / LPR, SLICES = C::EPI_WARPS * SUB, RC = 4, UNROLL = 4;
+      static_assert(2 * SLICES * RC * LPR * 16 <= 2 * C::P_BYTES, "two buffers of slices");
+      const int np = seg.last_cta - seg.first_cta + 1;
+      const int slice = warp * SUB + lane / LPR, l4 = lane % LPR;
+      auto sync = [&]() -> bool {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.joined);
+        const bool done = warp_wait(&bar.joined, red_ph, abort_flag, ws, 336);
+        red_ph ^= 1;
+        return done;
+      };
+      int buf = 0;
+      for (int n0 = 0; n0 < rows; n0 += RC, buf ^= 1) {
+        float4* red = reinterpret_cast<float4*>(sP) + buf * (SLICES * RC * LPR);
+        float4 sum[RC];
+#pragma unroll
+        for (int i = 0; i < RC; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p0 = slice; p0 < np; p0 += SLICES * UNROLL) {
+          float4 x[UNROLL][RC];
+#pragma unroll
+          for (int u = 0; u < UNROLL; ++u) {
+            // the first part lies in its CTA's second place, the others in their CTA's first
+            const int p = p0 + u * SLICES;
+            const float* part = a.parts + static_cast<size_t>(2 * (seg.first_cta + p) + (p == 0)) * (NR * D) + 4 * l4;
+#pragma unroll
+            for (int i = 0; i < RC; ++i) {
+              x[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (p < np && n0 + i < rows) x[u][i] = __ldcg(reinterpret_cast<const float4*>(part + (n0 + i) * D));
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+            for (int i = 0; i < RC; ++i) {
+              sum[i].x += x[u][i].x;
+              sum[i].y += x[u][i].y;
+              sum[i].z += x[u][i].z;
+              sum[i].w += x[u][i].w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RC; ++i) red[(slice * RC + i) * LPR + l4] = sum[i];
+        if (!sync()) return false;
+        const int pair = warp * 32 + lane, i = pair / (D / 2), c = pair % (D / 2);
+        if (i < RC && n0 + i < rows) {
+          float2 s = make_float2(0.f, 0.f);
+          const float2* from = reinterpret_cast<const float2*>(red) + i * (D / 2) + c;
+          for (int k = 0; k < min(np, SLICES); ++k) {
+            const float2 x = from[k * RC * (D / 2)];
+            s.x += x.x;
+            s.y += x.y;
+          }
+          const int n = n0 + i;
+          reinterpret_cast<uint32_t*>(
+              a.o + (static_cast<size_t>(seg.start + n / G) * a.Hq + seg.head * G + n % G) * D)[c] = pack_bf16x2(s.x, s.y);
+        }
+      }
+      return sync();
+    };
     float* my_log2n = s_log2n[warp];
     int* my_seen = s_seen[warp];
     bool ok = true;
@@ -411,18 +457,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
         if (mine && n0 + i < rows) __stcg(part + (n0 + i) * D + dcol, __uint_as_float(o[i]));
       if (!(ok = last_part(&bar.stored, &bar.counted, &bar.last, seg, ws, warp, lane, parts, abort_flag, 334))) break;
       parts ^= 1;
-      if (bar.last) {
-        const int np = seg.last_cta - seg.first_cta + 1;
-        const float* from = a.parts + static_cast<size_t>(2 * seg.first_cta) * (NR * D) + dcol;
-        for (int i = 0; i < HR && n0 + i < rows; ++i) {
-          if (!mine) break;
-          // the first part lies in its CTA's second place, the others in their CTA's first
-          float sum = __ldcg(from + NR * D + (n0 + i) * D);
-#pragma unroll 8
-          for (int p = 1; p < np; ++p) sum += __ldcg(from + static_cast<size_t>(2 * p) * (NR * D) + (n0 + i) * D);
-          *out_at(n0 + i) = __float2bfloat16(sum);
-        }
-      }
+      if (bar.last && !(ok = join(seg, rows))) break;
     }
   }
 

@@ -92,6 +92,9 @@ __device__ __forceinline__ long long floor_sum(long long n, long long x, long lo
 struct TileMath {
   int item;  // tokens per item
   int causal;
+  __device__ __forceinline__ int blocks(const SeqInfo& s, int k) const {
+    return blocks(s.m, s.n, min((k + 1) * item, s.m) - 1);
+  }
   __device__ __forceinline__ int items(const SeqInfo& s) const { return (s.m + item - 1) / item; }
   // Keys that token i sees.
   __device__ __forceinline__ int seen(int m, int n, int i) const {
@@ -191,44 +194,10 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
     uint32_t st[2] = {0, 0}, ph[2] = {0, 0}, loads[2] = {0, 0};
     int q_last = -1;
     bool ok = true;
-    const PlanRun run = bar.run;
-    long long unit = run.first, left = run.count;
-    Segment seg{};
-    SeqInfo s{};
-    int items = 0;
-    auto begin_tile = [&]() {
-      seg.blocks = math.blocks(s.m, s.n, min((seg.tile + 1) * 2 * T, s.m) - 1);
-    };
-    auto begin_seq = [&]() {
-      seq_info(a, seg.b, &s);
-      items = math.items(s);
-      seg.start = s.start;
-      seg.m = s.m;
-      seg.n = s.n;
-    };
-    if (left > 0) {
-      seg.b = run.b;
-      begin_seq();
-      const long long each = math.before(s, items);
-      const long long rem = run.rem % each;
-      seg.head = static_cast<int>(run.rem / each);
-      int lo = 0, hi = items - 1;  // the last tile with before(tile) <= rem
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (math.before(s, mid) <= rem) lo = mid; else hi = mid - 1;
-      }
-      seg.tile = lo;
-      seg.j0 = static_cast<int>(rem - math.before(s, lo));
-      begin_tile();
-    }
-    while (ok && left > 0) {
-      const int len = static_cast<int>(min(left, static_cast<long long>(seg.blocks - seg.j0)));
-      seg.j1 = seg.j0 + len;
-      seg.first_cta = static_cast<int>((unit - seg.j0) / run.per);
-      seg.last_cta = static_cast<int>((unit - seg.j0 + seg.blocks - 1) / run.per);
-      seg.lead = static_cast<int>((unit - seg.j0) % run.per);
+    RunWalker<TileMath> walk(a, math, bar.run, lane);
+    const Segment& seg = walk.seg;
+    for (bool more = bar.run.count > 0; ok && more; more = ok && walk.next()) {
       if (!(ok = seg_publish(bar.ring, rst, rph, seg, lane, abort_flag, ws, 400))) break;
-      PageWindow pages(a, seg.b, seg.n, seg.j0 * kKeyBlock, lane);
       if (!(ok = warp_wait(&bar.q_empty, qph ^ 1, abort_flag, ws, 401))) break;
       if (lane == 0) {
         const int i0 = seg.tile * 2 * T, ntiles = i0 + T < seg.m ? 2 : 1;
@@ -244,7 +213,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         const int keys = min(kKeyBlock, seg.n - j * kKeyBlock);
         const int boxes = (keys + rb - 1) / rb;  // 0 for a sequence without keys
         int row;
-        const int z = pages.locate(a, j * kKeyBlock, lane / C::CH, rb, lane / C::CH < boxes, seg.head, &row);
+        const int z = walk.locate(j, lane / C::CH, rb, lane / C::CH < boxes, &row);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           uint64_t* full = kv ? &bar.v_full[st[1]] : &bar.k_full[st[0]];
@@ -260,27 +229,8 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
           if (++st[kv] == (kv ? C::VST : C::KST)) { st[kv] = 0; ph[kv] ^= 1; }
         }
       }
-      unit += len;
-      left -= len;
-      seg.j0 = 0;
-      if (left == 0) break;
-      if (++seg.tile == items) {
-        seg.tile = 0;
-        if (++seg.head == a.Hkv) {  // on to the next sequence with new tokens
-          seg.head = 0;
-          do {
-            ++seg.b;
-            begin_seq();
-          } while (s.m == 0 && seg.b + 1 < a.B);
-          if (s.m == 0) break;
-        }
-      }
-      begin_tile();
     }
-    if (ok) {
-      seg.j1 = -1;
-      ok = seg_publish(bar.ring, rst, rph, seg, lane, abort_flag, ws, 403);
-    }
+    if (ok) ok = seg_publish(bar.ring, rst, rph, end_segment(), lane, abort_flag, ws, 403);
     if (!ok) {  // aborting: let the copies in flight land before the CTA exits
       int never = 0;
       volatile int* no_abort = &never;
@@ -531,30 +481,47 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         if (!(ok = last_part(&bar.stored, &bar.counted, &bar.last, seg, ws, warp, lane, parts, abort_flag, 425))) break;
         parts ^= 1;
       }
-      if (!whole && bar.last && writes) {
-        // The first part lies in its CTA's second place, the others in their
-        // CTA's first. Parts that start past the tile's last block are not there.
-        const int all = math.blocks(seg.m, seg.n, min(token - ri + T, seg.m) - 1);
-        for (int c = 0; c < D / 16; ++c) {
-          float4 sum[2];
-          const float* from = a.parts + (2 * seg.first_cta + 1) * kPart + mine + c * 8;
-          for (int e = 0; e < 2; ++e) sum[e] = __ldcg(reinterpret_cast<const float4*>(from) + e);
-#pragma unroll 4
-          for (int p = 1; p <= seg.last_cta - seg.first_cta; ++p) {
-            if (p * bar.run.per - seg.lead >= all) break;
-            from = a.parts + static_cast<size_t>(2 * (seg.first_cta + p)) * kPart + mine + c * 8;
+      if (!whole && bar.last) {
+        // The sum of the tiles' parts. Lanes take four columns each, so a warp
+        // reads SUB rows of a part at once, and it reads RB such rows (all of one
+        // tile) before it adds any. The first part lies in its CTA's second
+        // place, the others in their CTA's first; parts that start past the
+        // tile's last block are not there.
+        constexpr int LPR = D / 4, SUB = 32 / LPR, STEP = C::EPI_WARPS * SUB, RB = 128 / STEP;
+        for (int u = 0; u < 2; ++u) {
+          const int u0 = seg.tile * 2 * T + u * T;
+          if (u0 >= seg.m) break;
+          const int all = math.blocks(seg.m, seg.n, min(u0 + T, seg.m) - 1);
+          const int row0 = warp * SUB + lane / LPR, used = min(T, seg.m - u0) * G;
+          const float* from = a.parts + (2 * seg.first_cta + 1) * kPart + (u * 128 + row0) * D + 4 * (lane % LPR);
+          float4 sum[RB];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(from) + e);
-              sum[e].x += x.x;
-              sum[e].y += x.y;
-              sum[e].z += x.z;
-              sum[e].w += x.w;
+          for (int k = 0; k < RB; ++k) sum[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int p = 0; p <= seg.last_cta - seg.first_cta; ++p) {
+            if (p > 0 && p * bar.run.per - seg.lead >= all) break;
+            float4 x[RB];
+#pragma unroll
+            for (int k = 0; k < RB; ++k) {
+              x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (row0 + k * STEP < used) x[k] = __ldcg(reinterpret_cast<const float4*>(from + k * STEP * D));
             }
+#pragma unroll
+            for (int k = 0; k < RB; ++k) {
+              sum[k].x += x[k].x;
+              sum[k].y += x[k].y;
+              sum[k].z += x[k].z;
+              sum[k].w += x[k].w;
+            }
+            from += (p == 0 ? 1 : 2) * kPart;
           }
-          *reinterpret_cast<uint4*>(dst + c * 8) =
-              make_uint4(pack_bf16x2(sum[0].x, sum[0].y), pack_bf16x2(sum[0].z, sum[0].w),
-                         pack_bf16x2(sum[1].x, sum[1].y), pack_bf16x2(sum[1].z, sum[1].w));
+#pragma unroll
+          for (int k = 0; k < RB; ++k) {
+            const int row = row0 + k * STEP;
+            if (row < used)
+              *reinterpret_cast<uint2*>(
+                  a.o + (static_cast<size_t>(seg.start + u0 + row / G) * a.Hq + seg.head * G + row % G) * D +
+                  4 * (lane % LPR)) = make_uint2(pack_bf16x2(sum[k].x, sum[k].y), pack_bf16x2(sum[k].z, sum[k].w));
+          }
         }
       }
       __syncwarp();

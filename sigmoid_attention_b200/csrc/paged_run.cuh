@@ -47,6 +47,7 @@ __device__ __forceinline__ bool seq_info(const PagedAttend& a, int b, SeqInfo* s
 // unit is unit `rem` of sequence b.
 struct PlanRun {
   long long first, count, per, rem;
+  SeqInfo s;
   int b;
 };
 
@@ -60,8 +61,8 @@ __device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun* run, Uni
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int chunk = ceil_div(a.B, THREADS);
   const int b0 = min(a.B, tid * chunk), b1 = min(a.B, b0 + chunk);
+  SeqInfo s;  // of the sequence that units_of saw last
   auto units_of = [&](int b, bool report) -> long long {
-    SeqInfo s;
     if (!seq_info(a, b, &s)) {
       if (report && blockIdx.x == 0) raise_invalid(a.ws, -(b + 1));
       return 0;
@@ -95,13 +96,14 @@ __device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun* run, Uni
   if (first >= base && first < base + mine) {
     long long rem = first - base;
     int b = b0;
-    for (;; ++b) {
+    for (; chunk > 1; ++b) {  // (a thread with one sequence still holds it)
       const long long u = units_of(b, false);
       if (rem < u) break;
       rem -= u;
     }
     run->b = b;
     run->rem = rem;
+    run->s = s;
   }
 }
 
@@ -114,6 +116,12 @@ struct Segment {
   int lead;  // the first CTA's units before the tile (a part p CTAs on starts at block p * per - lead)
 };
 static_assert(sizeof(Segment) == 48, "three int4");
+
+__device__ __forceinline__ Segment end_segment() {
+  Segment s{};
+  s.j1 = -1;
+  return s;
+}
 
 struct SegRing {
   static constexpr int kSlots = 4;
@@ -164,31 +172,146 @@ __device__ __forceinline__ void seg_release(SegRing& r, uint32_t& st, uint32_t& 
   if (++st == SegRing::kSlots) { st = 0; ph ^= 1; }
 }
 
-// The page numbers of the blocks a producer warp is about to load: lane l holds
-// table entry base + l, and the next 32 are on the way.
-struct PageWindow {
+// A producer warp's walk along its CTA's run. Lengths and page numbers come from
+// global memory: lane l holds the lengths of sequence base + l and the page
+// of table entry window + l, and the next ones (the following 32 sequences, the
+// following 32 entries, the next sequence's first 32 entries) are loaded long
+// before they are needed, so that only the run's first block waits for them.
+//
+// Tiles: items(s), blocks(s, tile) and before(s, k) (the blocks of tiles
+// 0 .. k - 1) of one key/value head of a sequence with new tokens.
+template <typename Tiles>
+struct RunWalker {
+  const PagedAttend& a;
+  const Tiles& tiles;
+  const int lane;
+  long long unit, left, per;
+  Segment seg;
+  SeqInfo s, next_s;
+  int items, next_b;
+  int seq_base;
+  SeqInfo seq_cur, seq_ahead;
   const int* row;
-  int base, pages, cur, next;
-  __device__ __forceinline__ int entry(int i, int lane) const { return i + lane < pages ? __ldcg(row + i + lane) : -1; }
-  __device__ __forceinline__ PageWindow(const PagedAttend& a, int b, int n, int key0, int lane)
-      : row(a.table + static_cast<size_t>(b) * a.max_pages), base(key0 >> a.page_shift),
-        pages((n + (1 << a.page_shift) - 1) >> a.page_shift) {
-    cur = entry(base, lane);
-    next = entry(base + 32, lane);
+  int pages, first, next_first, window, cur, ahead;
+
+  __device__ __forceinline__ SeqInfo load_seq(int b) const {
+    SeqInfo x{0, 0, 0};
+    if (b < a.B) seq_info(a, b, &x);
+    return x;
   }
-  // Where box `box` (of rb keys) of the block at key0 lies: the slice (page *
-  // Hkv + head) and *r, the row in it. A bad page (reported where `used`)
-  // lies past the last slice, where a load reads zeros. Blocks come in order.
-  __device__ __forceinline__ int locate(const PagedAttend& a, int key0, int box, int rb, bool used, int head, int* r) {
-    if ((key0 >> a.page_shift) >= base + 32) {
-      base += 32;
-      cur = next;
-      next = entry(base + 32, threadIdx.x & 31);
+  __device__ __forceinline__ SeqInfo from_lane(const SeqInfo& x, int l) const {
+    return SeqInfo{__shfl_sync(0xffffffffu, x.start, l), __shfl_sync(0xffffffffu, x.m, l),
+                   __shfl_sync(0xffffffffu, x.n, l)};
+  }
+  // Find the next sequence after b with new tokens (a.B: none) and start the
+  // load of its first page numbers.
+  __device__ __forceinline__ void look_ahead(int b) {
+    for (;;) {
+      const int from = b + 1 - seq_base;  // 1 .. 32
+      unsigned found = __ballot_sync(0xffffffffu, seq_cur.m > 0);
+      found = from < 32 ? found >> from << from : 0u;
+      if (found) {
+        next_b = seq_base + __ffs(found) - 1;
+        next_s = from_lane(seq_cur, next_b - seq_base);
+        next_first = entry(a.table + static_cast<size_t>(next_b) * a.max_pages, pages_of(next_s.n), 0);
+        return;
+      }
+      seq_base += 32;
+      if (seq_base >= a.B) break;
+      seq_cur = seq_ahead;
+      seq_ahead = load_seq(seq_base + 32 + lane);
+      b = seq_base - 1;
     }
-    const int key = key0 + box * rb;
-    const int page = __shfl_sync(0xffffffffu, cur, ((key >> a.page_shift) - base) & 31);
+    next_b = a.B;
+  }
+  __device__ __forceinline__ int pages_of(int n) const { return (n + (1 << a.page_shift) - 1) >> a.page_shift; }
+  __device__ __forceinline__ int entry(const int* r, int count, int i) const {
+    return i + lane < count ? __ldcg(r + i + lane) : -1;
+  }
+  __device__ __forceinline__ void enter() {
+    seg.start = s.start;
+    seg.m = s.m;
+    seg.n = s.n;
+    row = a.table + static_cast<size_t>(seg.b) * a.max_pages;
+    pages = pages_of(s.n);
+    items = tiles.items(s);
+  }
+
+  __device__ __forceinline__ RunWalker(const PagedAttend& args, const Tiles& t, const PlanRun& run, int ln)
+      : a(args), tiles(t), lane(ln), unit(run.first), left(run.count), per(run.per) {
+    if (left <= 0) return;
+    s = run.s;
+    seg = Segment{};
+    seg.b = run.b;
+    enter();
+    first = entry(row, pages, 0);
+    seq_base = seg.b;
+    seq_cur = load_seq(seq_base + lane);
+    seq_ahead = load_seq(seq_base + 32 + lane);
+    const long long each = tiles.before(s, items);
+    const long long rem = run.rem % each;
+    seg.head = static_cast<int>(run.rem / each);
+    int lo = 0, hi = items - 1;  // the last tile with before(tile) <= rem
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (tiles.before(s, mid) <= rem) lo = mid; else hi = mid - 1;
+    }
+    seg.tile = lo;
+    seg.j0 = static_cast<int>(rem - tiles.before(s, lo));
+    seg.blocks = tiles.blocks(s, lo);
+    open();
+    look_ahead(seg.b);
+  }
+
+  // The segment that starts at seg.j0 (left > 0).
+  __device__ __forceinline__ void open() {
+    const int len = static_cast<int>(min(left, static_cast<long long>(seg.blocks - seg.j0)));
+    const long long tile_unit = unit - seg.j0;  // the tile's first unit
+    seg.j1 = seg.j0 + len;
+    seg.first_cta = static_cast<int>(tile_unit / per);
+    seg.last_cta = static_cast<int>((tile_unit + seg.blocks - 1) / per);
+    seg.lead = static_cast<int>(tile_unit - seg.first_cta * per);
+    unit += len;
+    left -= len;
+    window = ((seg.j0 * kKeyBlock) >> a.page_shift) & ~31;
+    cur = window == 0 ? first : entry(row, pages, window);
+    ahead = entry(row, pages, window + 32);
+  }
+
+  // On to the run's next segment; false at its end.
+  __device__ __forceinline__ bool next() {
+    if (left <= 0) return false;
+    seg.j0 = 0;
+    if (++seg.tile == items) {
+      seg.tile = 0;
+      if (++seg.head == a.Hkv) {  // the next sequence
+        seg.head = 0;
+        if (next_b >= a.B) return false;
+        s = next_s;
+        seg.b = next_b;
+        first = next_first;
+        enter();
+        look_ahead(seg.b);
+      }
+    }
+    seg.blocks = tiles.blocks(s, seg.tile);
+    open();
+    return true;
+  }
+
+  // Where box `box` (of rb keys) of block j lies: the slice (page * Hkv + head)
+  // and *r, the row in it. A bad page (reported where `used`) lies past the last
+  // slice, where a load reads zeros. Blocks come in order.
+  __device__ __forceinline__ int locate(int j, int box, int rb, bool used, int* r) {
+    if (((j * kKeyBlock) >> a.page_shift) >= window + 32) {
+      window += 32;
+      cur = ahead;
+      ahead = entry(row, pages, window + 32);
+    }
+    const int key = j * kKeyBlock + box * rb;
+    const int page = __shfl_sync(0xffffffffu, cur, (key >> a.page_shift) & 31);
     *r = key & ((1 << a.page_shift) - 1);
-    if (page >= 0 && page < a.num_pages) return page * a.Hkv + head;
+    if (page >= 0 && page < a.num_pages) return page * a.Hkv + seg.head;
     if (used) raise_invalid(a.ws, 203);
     return a.num_pages * a.Hkv;
   }
