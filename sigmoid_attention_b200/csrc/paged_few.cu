@@ -25,9 +25,18 @@
 //    epilogue thread owns one key: its NR weights go to shared memory as one
 //    row of the second product's B operand.
 //
-// Roles (11 warps): 0-7 epilogue in two groups of four that take blocks in
-// turn (thread = key), 8 the producer (plan, page tables, TMA), 9 the issuer of
-// S^T, 10 the issuer of O^T.
+//  * A thread issues a tcgen05.mma only about every 100 cycles, so a block's
+//    eight O^T products cost 1400 cycles with their waits, which is what a
+//    block of D = 64 takes to arrive. Blocks therefore alternate between two
+//    groups, each with its own S^T region, P buffer, issuer and O^T
+//    accumulator; a segment's two accumulators are added when it is read out.
+//  * Reading a segment out (and joining a cut tile) is the work of four more
+//    warps, so the next segment's weights do not wait for it: short texts
+//    took 4200 cycles per segment before, most of them this chain.
+//
+// Roles (16 warps): 0-7 weights, four per group (thread = key), 8-11 output
+// (thread = column of O), 12 the producer (page tables, TMA), 13 the issuer of
+// S^T, 14 and 15 the groups' issuers of O^T.
 #include "paged_run.cuh"
 
 namespace sigattn {
@@ -51,14 +60,19 @@ struct FewCfg {
   static constexpr int P_BYTES = kKeyBlock * 128;      // rows of 64 columns, NR of them in use
   static constexpr int OFF_P = STAGES * TILE_BYTES;
   static constexpr int OFF_Q = OFF_P + 2 * P_BYTES;
-  static constexpr int SMEM_ALLOC = OFF_Q + 2 * Q_BYTES + 1024;
+  static constexpr int OFF_RED = OFF_Q + 2 * Q_BYTES;   // slices' sums of four rows of a join
+  static constexpr int LPR = D / 4, SUB = 32 / LPR;     // lanes per row of a part, rows a warp reads at once
+  static constexpr int OUT_WARPS = 4;
+  static constexpr int SLICES = OUT_WARPS * SUB, RC = 4;
+  static constexpr int RED_BYTES = SLICES * RC * LPR * 16;
+  static constexpr int SMEM_ALLOC = OFF_RED + RED_BYTES + 1024;
   static_assert(SMEM_ALLOC <= 220 * 1024, "shared memory budget");
-  static constexpr int TM_S = 0;                        // two S^T regions, then two O^T regions
+  static constexpr int TM_S = 0;                        // two S^T regions, then two O^T pairs
   static constexpr int TM_O = 2 * NR;
-  static constexpr int TMEM_COLS = 4 * NR;
+  static constexpr int TMEM_COLS = NR == 16 ? 128 : NR == 32 ? 256 : 512;  // >= 6 NR
   static constexpr int EPI_WARPS = 8;
-  static constexpr int WARPS = EPI_WARPS + 3;
-  static constexpr int THREADS = WARPS * 32;
+  static constexpr int kProducer = EPI_WARPS + OUT_WARPS, kIssueS = kProducer + 1, kIssueO = kProducer + 2;
+  static constexpr int THREADS = (kIssueO + 2) * 32;
 };
 
 // All new tokens of a sequence make one tile.
@@ -77,7 +91,7 @@ struct FewBarriers {
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full[2], p_empty[2];
   uint64_t o_full[2], o_empty[2];
-  uint64_t stored, counted, joined, drain[2];
+  uint64_t stored, counted, joined, drain[3];
   SegRing ring;
   PlanRun run;
   uint32_t tmem_base;
@@ -101,12 +115,12 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &bar.abort;
   int* ws = a.ws;
-  constexpr int kProducer = C::EPI_WARPS, kIssueS = kProducer + 1, kIssueO = kProducer + 2;
+  constexpr int kProducer = C::kProducer, kIssueS = C::kIssueS, kIssueO = C::kIssueO;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&bar.full[s], 1);
-      mbar_init(&bar.empty[s], 1);
+      mbar_init(&bar.empty[s], s < C::KST ? 1 : 2);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.q_full[s], 1);
@@ -115,14 +129,14 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
       mbar_init(&bar.s_empty[s], 4);
       mbar_init(&bar.p_full[s], 4);
       mbar_init(&bar.p_empty[s], 1);
-      mbar_init(&bar.o_full[s], 1);
-      mbar_init(&bar.o_empty[s], C::EPI_WARPS);
-      mbar_init(&bar.drain[s], 1);
+      mbar_init(&bar.o_full[s], 2);
+      mbar_init(&bar.o_empty[s], C::OUT_WARPS);
     }
-    mbar_init(&bar.stored, C::EPI_WARPS);
+    for (int s = 0; s < 3; ++s) mbar_init(&bar.drain[s], 1);
+    mbar_init(&bar.stored, C::OUT_WARPS);
     mbar_init(&bar.counted, 1);
-    mbar_init(&bar.joined, C::EPI_WARPS);
-    seg_ring_init(bar.ring, C::EPI_WARPS + 2);
+    mbar_init(&bar.joined, C::OUT_WARPS);
+    seg_ring_init(bar.ring, C::EPI_WARPS + C::OUT_WARPS + 3);
     bar.abort = 0;
     fence_mbar_init();
   }
@@ -237,14 +251,17 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
       mma_commit(&bar.drain[0]);
       mbar_wait(&bar.drain[0], 0, &never, ws, 319);
     }
-  } else if (warp == kIssueO) {
-    // ------------------------------------------- O^T += V^T P^T (D x NR)
-    // At D = 64 the product's 128 rows hold V's 64 columns twice (the second
-    // column block's distance is 0); the second half is not read.
+  } else if (warp >= kIssueO) {
+    // -------------------------------- O^T += V^T P^T (D x NR), group g's blocks
+    // Both issuers wait for every V tile and release it (so each sees every
+    // phase of a slot); the block's group uses it. At D = 64 the product's 128 rows
+    // hold V's 64 columns twice (the second column block's distance is 0); the
+    // second half is not read.
+    const uint32_t g = warp - kIssueO;
     constexpr uint32_t idesc = idesc_bf16_f32(128, NR, true, true);
     const uint64_t d_v = smem_desc_sw128(smem_u32(smem), D == 64 ? 0 : C::BOX_BYTES, 1024);
-    const uint64_t d_p = smem_desc_sw128(smem_u32(sP), C::P_BYTES, 1024);
-    uint32_t st = C::KST, ph = 0, pb = 0, pph = 0, ob = 0, oph = 0, rst = 0, rph = 0;
+    const uint64_t d_p = smem_desc_sw128(smem_u32(sP), C::P_BYTES, 1024) + ((g * C::P_BYTES) >> 4);
+    uint32_t st = C::KST, ph = 0, t = 0, pph = 0, ob = 0, oph = 0, rst = 0, rph = 0;
     bool ok = true;
     while (ok) {
       Segment seg;
@@ -252,120 +269,69 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
       __syncwarp();
       seg_release(bar.ring, rst, rph, lane == 0);
       if (seg.j1 < 0) break;
-      for (int j = seg.j0; j < seg.j1; ++j) {
+      if (!(ok = warp_wait(&bar.o_empty[ob], oph ^ 1, abort_flag, ws, 323))) break;
+      const uint32_t tm_o = tmem + C::TM_O + (2 * ob + g) * NR;
+      uint32_t fresh = 0;  // 1 once the segment's accumulator holds a product
+      for (int j = seg.j0; j < seg.j1; ++j, ++t) {
         if (!(ok = warp_wait(&bar.full[st], ph, abort_flag, ws, 321))) break;
-        // The product takes keys in sixteens. Rows of V past the text's end in
-        // the last sixteen hold whatever the page (or an earlier tile) held;
-        // their weights are 0, and 0 * NaN must not be: they are zeroed.
-        const int keys = min(kKeyBlock, seg.n - j * kKeyBlock);
-        const int steps = max(1, (keys + 15) / 16);
-        if (keys < steps * 16) {
-          uint4* v = reinterpret_cast<uint4*>(smem + st * C::TILE_BYTES);
-          for (int i = lane; i < (steps * 16 - keys) * 8; i += 32)
-            for (int c = 0; c < C::CH; ++c) v[(c * C::BOX_BYTES + keys * 128) / 16 + i] = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
+        if ((t & 1) == g) {
+          // The product takes keys in sixteens. Rows of V past the text's end in
+          // the last sixteen hold whatever the page (or an earlier tile) held;
+          // their weights are 0, and 0 * NaN must not be: they are zeroed.
+          const int keys = min(kKeyBlock, seg.n - j * kKeyBlock);
+          const int steps = max(1, (keys + 15) / 16);
+          if (keys < steps * 16) {
+            uint4* v = reinterpret_cast<uint4*>(smem + st * C::TILE_BYTES);
+            for (int i = lane; i < (steps * 16 - keys) * 8; i += 32)
+              for (int c = 0; c < C::CH; ++c) v[(c * C::BOX_BYTES + keys * 128) / 16 + i] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (!(ok = warp_wait(&bar.p_full[g], pph, abort_flag, ws, 322))) break;
+          pph ^= 1;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t v0 = d_v + ((st * C::TILE_BYTES) >> 4);
+            mma_ss(tm_o, v0, d_p, idesc, fresh);
+            if (steps == 8) {
+#pragma unroll
+              for (int kk = 1; kk < 8; ++kk) mma_ss(tm_o, v0 + ((kk * 2048) >> 4), d_p + ((kk * 2048) >> 4), idesc, 1u);
+            } else {
+              for (int kk = 1; kk < steps; ++kk) mma_ss(tm_o, v0 + ((kk * 2048) >> 4), d_p + ((kk * 2048) >> 4), idesc, 1u);
+            }
+            mma_commit(&bar.empty[st]);
+            mma_commit(&bar.p_empty[g]);
+          }
           __syncwarp();
+          fresh = 1;
+        } else if (lane == 0) {
+          mbar_arrive(&bar.empty[st]);
         }
-        if (!(ok = warp_wait(&bar.p_full[pb], pph, abort_flag, ws, 322))) break;
-        if (j == seg.j0 && !(ok = warp_wait(&bar.o_empty[ob], oph ^ 1, abort_flag, ws, 323))) break;
-        tc_fence_after();
-        if (lane == 0) {
-          for (int kk = 0; kk < steps; ++kk)
-            mma_ss(tmem + C::TM_O + ob * NR, d_v + ((st * C::TILE_BYTES + kk * 2048) >> 4),
-                   d_p + ((pb * C::P_BYTES + kk * 2048) >> 4), idesc, (j > seg.j0 || kk > 0) ? 1u : 0u);
-          mma_commit(&bar.empty[st]);
-          mma_commit(&bar.p_empty[pb]);
-          if (j + 1 == seg.j1) mma_commit(&bar.o_full[ob]);
-        }
-        __syncwarp();
-        if ((pb ^= 1) == 0) pph ^= 1;
         if (++st == C::STAGES) { st = C::KST; ph ^= 1; }
       }
+      if (!ok) break;
+      if (lane == 0) mma_commit(&bar.o_full[ob]);
+      __syncwarp();
       if ((ob ^= 1) == 0) oph ^= 1;
     }
     if (lane == 0) {
       int never = 0;
-      mma_commit(&bar.drain[1]);
-      mbar_wait(&bar.drain[1], 0, &never, ws, 329);
+      mma_commit(&bar.drain[1 + g]);
+      mbar_wait(&bar.drain[1 + g], 0, &never, ws, 329);
     }
     __syncwarp();
-  } else {
-    // ------------------------------------------------------------- epilogue
+  } else if (warp < C::EPI_WARPS) {
+    // -------------------------------------------------------------- weights
     const int g = warp >> 2;                       // this group's blocks, S region and P buffer
     const int quad = warp & 3;
     const int key = (quad << 5) + lane;            // key within the block = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quad << 5) << 16;
     constexpr float scale_l2e = Scale<D>::value * kLog2e;
     uint8_t* prow = sP + g * C::P_BYTES + key * 128;
-    uint32_t t = 0, sph = 0, pph = 0, ob = 0, oph = 0, rst = 0, rph = 0, parts = 0;
-    // The sum of a tile's parts, by all epilogue warps: `rows` rows of D, four at
-    // a time. Lanes take four columns each, so a warp reads SUB rows of a part
-    // at once; part p belongs to slice p % SLICES, the slices are added in order.
-    // The P buffers hold the slices' sums: every product that reads them has
-    // completed, and the next weights are written after the last barrier below.
-    uint32_t red_ph = 0;
-    auto join = [&](const Segment& seg, int rows) -> bool {
-      constexpr int LPR = D / 4, SUB = 32 / LPR, SLICES = C::EPI_WARPS * SUB, RC = 4, UNROLL = 4;
-      static_assert(2 * SLICES * RC * LPR * 16 <= 2 * C::P_BYTES, "two buffers of slices");
-      const int np = seg.last_cta - seg.first_cta + 1;
-      const int slice = warp * SUB + lane / LPR, l4 = lane % LPR;
-      auto sync = [&]() -> bool {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.joined);
-        const bool done = warp_wait(&bar.joined, red_ph, abort_flag, ws, 336);
-        red_ph ^= 1;
-        return done;
-      };
-      int buf = 0;
-      for (int n0 = 0; n0 < rows; n0 += RC, buf ^= 1) {
-        float4* red = reinterpret_cast<float4*>(sP) + buf * (SLICES * RC * LPR);
-        float4 sum[RC];
-#pragma unroll
-        for (int i = 0; i < RC; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p0 = slice; p0 < np; p0 += SLICES * UNROLL) {
-          float4 x[UNROLL][RC];
-#pragma unroll
-          for (int u = 0; u < UNROLL; ++u) {
-            // the first part lies in its CTA's second place, the others in their CTA's first
-            const int p = p0 + u * SLICES;
-            const float* part = a.parts + static_cast<size_t>(2 * (seg.first_cta + p) + (p == 0)) * (NR * D) + 4 * l4;
-#pragma unroll
-            for (int i = 0; i < RC; ++i) {
-              x[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (p < np && n0 + i < rows) x[u][i] = __ldcg(reinterpret_cast<const float4*>(part + (n0 + i) * D));
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < UNROLL; ++u)
-#pragma unroll
-            for (int i = 0; i < RC; ++i) {
-              sum[i].x += x[u][i].x;
-              sum[i].y += x[u][i].y;
-              sum[i].z += x[u][i].z;
-              sum[i].w += x[u][i].w;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < RC; ++i) red[(slice * RC + i) * LPR + l4] = sum[i];
-        if (!sync()) return false;
-        const int pair = warp * 32 + lane, i = pair / (D / 2), c = pair % (D / 2);
-        if (i < RC && n0 + i < rows) {
-          float2 s = make_float2(0.f, 0.f);
-          const float2* from = reinterpret_cast<const float2*>(red) + i * (D / 2) + c;
-          for (int k = 0; k < min(np, SLICES); ++k) {
-            const float2 x = from[k * RC * (D / 2)];
-            s.x += x.x;
-            s.y += x.y;
-          }
-          const int n = n0 + i;
-          reinterpret_cast<uint32_t*>(
-              a.o + (static_cast<size_t>(seg.start + n / G) * a.Hq + seg.head * G + n % G) * D)[c] = pack_bf16x2(s.x, s.y);
-        }
-      }
-      return sync();
-    };
+    uint32_t t = 0, sph = 0, pph = 0, rst = 0, rph = 0;
     float* my_log2n = s_log2n[warp];
     int* my_seen = s_seen[warp];
+    const int token0 = lane / G, token1 = (lane + 32) / G;  // tokens of the columns this lane prepares
     bool ok = true;
     while (ok) {
       Segment seg;
@@ -375,14 +341,14 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
       if (seg.j1 < 0) break;
       // N and log2 N of each row (column of S^T); rows past the last see nothing.
       const int rows = seg.m * G;
-      int least = seg.n;
+#pragma unroll
       for (int n = lane; n < NR; n += 32) {
         int seen = seg.n;
-        if (a.causal) seen = max(0, min(seg.n, seg.n - seg.m + n / G + 1));
+        if (a.causal) seen = max(0, min(seg.n, seg.n - seg.m + (n < 32 ? token0 : token1) + 1));
         my_seen[n] = n < rows ? seen : 0;
-        my_log2n[n] = log2f(static_cast<float>(max(seen, 1)));
+        my_log2n[n] = __log2f(static_cast<float>(max(seen, 1)));
       }
-      if (a.causal) least = max(0, seg.n - seg.m + 1);
+      const int least = a.causal ? max(0, seg.n - seg.m + 1) : seg.n;  // keys that every row sees
       __syncwarp();
       for (int j = seg.j0; j < seg.j1; ++j, ++t) {
         if ((t & 1) != static_cast<uint32_t>(g)) continue;
@@ -429,33 +395,128 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
         sph ^= 1;
         pph ^= 1;
       }
-      if (!ok) break;
-      // O^T: thread = column d of the output, the group's half of the rows.
+    }
+  } else {
+    // --------------------------------------------------------------- output
+    const int ow = warp - C::EPI_WARPS;            // lane quadrant
+    const int dcol = (ow << 5) + lane;             // column of O = TMEM lane
+    const bool mine = D == 128 || dcol < D;
+    const uint32_t lane_off = static_cast<uint32_t>(ow << 5) << 16;
+    uint32_t t = 0, ob = 0, oph = 0, rst = 0, rph = 0, parts = 0, red_ph = 0;
+    bool ok = true;
+    auto sync = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.joined);
+      const bool done = warp_wait(&bar.joined, red_ph, abort_flag, ws, 336);
+      red_ph ^= 1;
+      return done;
+    };
+    // The sum of a tile's parts, by the output warps: `rows` rows of D, four at a
+    // time. Lanes take four columns each, so a warp reads SUB rows of a part at
+    // once; part p belongs to slice p % SLICES, the slices are added in order.
+    auto join = [&](const Segment& seg, int rows) -> bool {
+      constexpr int LPR = C::LPR, SLICES = C::SLICES, RC = C::RC, UNROLL = 4;
+      const int np = seg.last_cta - seg.first_cta + 1;
+      const int slice = ow * C::SUB + lane / LPR, l4 = lane % LPR;
+      float4* red = reinterpret_cast<float4*>(smem + C::OFF_RED);
+      for (int n0 = 0; n0 < rows; n0 += RC) {
+        float4 sum[RC];
+#pragma unroll
+        for (int i = 0; i < RC; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p0 = slice; p0 < np; p0 += SLICES * UNROLL) {
+          float4 x[UNROLL][RC];
+#pragma unroll
+          for (int u = 0; u < UNROLL; ++u) {
+            // the first part lies in its CTA's second place, the others in their CTA's first
+            const int p = p0 + u * SLICES;
+            const float* part = a.parts + static_cast<size_t>(2 * (seg.first_cta + p) + (p == 0)) * (NR * D) + 4 * l4;
+#pragma unroll
+            for (int i = 0; i < RC; ++i) {
+              x[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (p < np && n0 + i < rows) x[u][i] = __ldcg(reinterpret_cast<const float4*>(part + (n0 + i) * D));
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+            for (int i = 0; i < RC; ++i) {
+              sum[i].x += x[u][i].x;
+              sum[i].y += x[u][i].y;
+              sum[i].z += x[u][i].z;
+              sum[i].w += x[u][i].w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RC; ++i) red[(slice * RC + i) * LPR + l4] = sum[i];
+        if (!sync()) return false;
+        for (int pair = ow * 32 + lane; pair < RC * D / 2; pair += C::OUT_WARPS * 32) {
+          const int n = n0 + pair / (D / 2), c = pair % (D / 2);
+          if (n >= rows) break;
+          float2 s = make_float2(0.f, 0.f);
+          const float2* from = reinterpret_cast<const float2*>(red) + pair;
+          for (int k = 0; k < min(np, SLICES); ++k) {
+            const float2 x = from[k * RC * (D / 2)];
+            s.x += x.x;
+            s.y += x.y;
+          }
+          reinterpret_cast<uint32_t*>(
+              a.o + (static_cast<size_t>(seg.start + n / G) * a.Hq + seg.head * G + n % G) * D)[c] = pack_bf16x2(s.x, s.y);
+        }
+        if (!sync()) return false;
+      }
+      return true;
+    };
+    while (ok) {
+      Segment seg;
+      if (!(ok = seg_read<true>(bar.ring, rst, rph, &seg, abort_flag, ws, 340))) break;
+      __syncwarp();
+      seg_release(bar.ring, rst, rph, lane == 0);
+      if (seg.j1 < 0) break;
+      const int rows = seg.m * G, len = seg.j1 - seg.j0;
+      // Which groups had blocks of this segment.
+      const bool both = len > 1;
+      const uint32_t only = t & 1;
+      t += len;
       if (!(ok = warp_wait(&bar.o_full[ob], oph, abort_flag, ws, 333))) break;
       tc_fence_after();
-      constexpr int HR = NR / 2;
-      uint32_t o[HR];
-      tmem_ld_cols(tmem + lane_off + C::TM_O + ob * NR + g * HR, o);
+      const bool whole = len == seg.blocks;
+      __nv_bfloat16* dst = a.o + (static_cast<size_t>(seg.start) * a.Hq + seg.head * G) * D + dcol;
+      float* part = a.parts + static_cast<size_t>(2 * blockIdx.x + (seg.j0 == 0)) * (NR * D) + dcol;
+      int head = 0;
+#pragma unroll
+      for (int c = 0; c < NR / 16; ++c) {
+        if (16 * c >= rows) break;
+        uint32_t x[16];
+        const uint32_t from = tmem + lane_off + C::TM_O + 2 * ob * NR + 16 * c;
+        tmem_ld16(from + (both ? 0 : only * NR), x);
+        if (both) {
+          uint32_t y[16];
+          tmem_ld16(from + NR, y);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) + __uint_as_float(y[i]));
+        }
+        if (!mine) continue;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (16 * c + i >= rows) break;
+          if (whole) {
+            *dst = __float2bfloat16(__uint_as_float(x[i]));
+            dst += D;
+            if (++head == G) {  // on to the next token's first head
+              head = 0;
+              dst += static_cast<size_t>(a.Hq - G) * D;
+            }
+          } else {
+            __stcg(part + (16 * c + i) * D, __uint_as_float(x[i]));
+          }
+        }
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.o_empty[ob]);
       if ((ob ^= 1) == 0) oph ^= 1;
-      const int n0 = g * HR, dcol = key;
-      const bool mine = D == 128 || dcol < D;
-      auto out_at = [&](int n) {
-        return a.o + (static_cast<size_t>(seg.start + n / G) * a.Hq + seg.head * G + n % G) * D + dcol;
-      };
-      if (seg.j0 == 0 && seg.j1 == seg.blocks) {
-#pragma unroll
-        for (int i = 0; i < HR; ++i)
-          if (mine && n0 + i < rows) *out_at(n0 + i) = __float2bfloat16(__uint_as_float(o[i]));
-        continue;
-      }
-      float* part = a.parts + static_cast<size_t>(2 * blockIdx.x + (seg.j0 == 0)) * (NR * D);
-#pragma unroll
-      for (int i = 0; i < HR; ++i)
-        if (mine && n0 + i < rows) __stcg(part + (n0 + i) * D + dcol, __uint_as_float(o[i]));
-      if (!(ok = last_part(&bar.stored, &bar.counted, &bar.last, seg, ws, warp, lane, parts, abort_flag, 334))) break;
+      if (whole) continue;
+      if (!(ok = last_part(&bar.stored, &bar.counted, &bar.last, seg, ws, ow, lane, parts, abort_flag, 334))) break;
       parts ^= 1;
       if (bar.last && !(ok = join(seg, rows))) break;
     }

@@ -43,6 +43,13 @@ __device__ __forceinline__ bool seq_info(const PagedAttend& a, int b, SeqInfo* s
   return ok;
 }
 
+// x / y and x % y of nonnegative numbers: unit counts nearly always fit 32 bits,
+// where a division takes a fraction of the time.
+__device__ __forceinline__ long long fast_div(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+
 // A CTA's run: units [first, first + count), `per` units to a CTA; its first
 // unit is unit `rem` of sequence b.
 struct PlanRun {
@@ -86,7 +93,7 @@ __device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun* run, Uni
     total += sums[w];
   }
   base += incl - mine;
-  const long long per = max(static_cast<long long>(a.least), (total + gridDim.x - 1) / gridDim.x);
+  const long long per = max(static_cast<long long>(a.least), fast_div(total + gridDim.x - 1, gridDim.x));
   const long long first = min(total, per * blockIdx.x);
   if (tid == 0) {
     run->first = first;
@@ -249,8 +256,8 @@ struct RunWalker {
     seq_cur = load_seq(seq_base + lane);
     seq_ahead = load_seq(seq_base + 32 + lane);
     const long long each = tiles.before(s, items);
-    const long long rem = run.rem % each;
-    seg.head = static_cast<int>(run.rem / each);
+    seg.head = static_cast<int>(fast_div(run.rem, each));
+    const long long rem = run.rem - seg.head * each;
     int lo = 0, hi = items - 1;  // the last tile with before(tile) <= rem
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -260,7 +267,7 @@ struct RunWalker {
     seg.j0 = static_cast<int>(rem - tiles.before(s, lo));
     seg.blocks = tiles.blocks(s, lo);
     open();
-    look_ahead(seg.b);
+    next_b = -1;  // looked for when the run's first loads are on their way
   }
 
   // The segment that starts at seg.j0 (left > 0).
@@ -268,8 +275,10 @@ struct RunWalker {
     const int len = static_cast<int>(min(left, static_cast<long long>(seg.blocks - seg.j0)));
     const long long tile_unit = unit - seg.j0;  // the tile's first unit
     seg.j1 = seg.j0 + len;
-    seg.first_cta = static_cast<int>(tile_unit / per);
-    seg.last_cta = static_cast<int>((tile_unit + seg.blocks - 1) / per);
+    const long long me = blockIdx.x;
+    const bool here = tile_unit >= me * per && tile_unit + seg.blocks <= (me + 1) * per;  // the tile lies in this run
+    seg.first_cta = here ? static_cast<int>(me) : static_cast<int>(fast_div(tile_unit, per));
+    seg.last_cta = here ? static_cast<int>(me) : static_cast<int>(fast_div(tile_unit + seg.blocks - 1, per));
     seg.lead = static_cast<int>(tile_unit - seg.first_cta * per);
     unit += len;
     left -= len;
@@ -281,6 +290,7 @@ struct RunWalker {
   // On to the run's next segment; false at its end.
   __device__ __forceinline__ bool next() {
     if (left <= 0) return false;
+    if (next_b < 0) look_ahead(seg.b);
     seg.j0 = 0;
     if (++seg.tile == items) {
       seg.tile = 0;
