@@ -79,6 +79,7 @@ struct FewCfg {
 struct OneTile {
   __device__ __forceinline__ int items(const SeqInfo&) const { return 1; }
   __device__ __forceinline__ int blocks(const SeqInfo& s, int) const { return seq_blocks(s.n); }
+  __device__ __forceinline__ int weight(const SeqInfo&, int) const { return 1; }
   __device__ __forceinline__ long long before(const SeqInfo& s, int k) const {
     return static_cast<long long>(k) * seq_blocks(s.n);
   }
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     const OneTile tiles{};
     RunWalker<OneTile> walk(a, tiles, bar.run, lane);
     const Segment& seg = walk.seg;
-    for (bool more = bar.run.count > 0; ok && more; more = ok && walk.next()) {
+    for (; ok && walk.alive; walk.next()) {
       if (!(ok = seg_publish(bar.ring, rst, rph, seg, lane, abort_flag, ws, 300))) break;
       if (!(ok = warp_wait(&bar.q_empty[qb], qph ^ 1, abort_flag, ws, 301))) break;
       if (lane == 0) {

@@ -19,6 +19,11 @@
 //    tiles over long texts are cut along the keys, and the causal triangle's
 //    uneven tiles need no other balancing. Parts are fp32 sums, added in CTA
 //    order by the CTA that stores last.
+//  * Where a segment has one tile only (a single token beside other users'
+//    prompts, a short chunk), its blocks alternate between the two tiles' S and
+//    P regions and epilogue warps ("dual"): a lone tile would wait through the
+//    chain S, weights, PV on every block. Issuer 0 then issues all products, so
+//    that all of them add to one O in order.
 //
 // Roles (19 warps): 0-15 epilogue (warps 0-7 tile 0, 8-15 tile 1; per tile, four
 // warps for each half of a block's keys), 16 the producer, 17 and 18 the
@@ -38,7 +43,8 @@ struct ManyCfg {
   static constexpr int VST = (D == 128) ? 2 : 3;
   static constexpr int BOX_BYTES = 128 * 128;
   static constexpr int TILE_BYTES = CH * BOX_BYTES;
-  static constexpr int OFF_K = 2 * TILE_BYTES;
+  static constexpr int QST = (D == 128) ? 3 : 4;  // query tiles: the next segment's are loaded ahead
+  static constexpr int OFF_K = QST * TILE_BYTES;
   static constexpr int OFF_V = OFF_K + KST * TILE_BYTES;
   static constexpr int SMEM_ALLOC = OFF_V + VST * TILE_BYTES + 1024;
   static constexpr bool SEP_P = (D == 64);
@@ -48,15 +54,16 @@ struct ManyCfg {
   static constexpr int THREADS = (EPI_WARPS + 3) * 32;
 };
 
-template <int KST, int VST>
+template <int QST, int KST, int VST>
 struct ManyBarriers {
-  uint64_t q_full, q_empty;
+  uint64_t q_full[QST], q_empty[QST];
   uint64_t k_full[KST], k_empty[KST];
   uint64_t v_full[VST], v_empty[VST];
   uint64_t s_full[2], p_full[4], o_full[2], o_empty[2];
   uint64_t epi_done[2];  // tile t's warps finished their pass over a block (d = 128: the tiles take turns)
   uint64_t s_read[2];    // SEP_P: the epilogue copied tile t's S out of TMEM
   uint64_t pv_done[2];   // SEP_P: tile t's PV products of a block completed (P region free)
+  uint64_t fin[2][4];    // issuer t's products of a segment completed (by segment, modulo 4)
   uint64_t stored, counted, drain[2];
   SegRing ring;
   PlanRun run;
@@ -64,59 +71,73 @@ struct ManyBarriers {
   int abort, last;
 };
 
-// sum_{k < n} floor((x k + y) / 128), x and y >= 0: after taking out whole
-// parts, the lattice points under the line are counted along the other axis.
-__device__ __forceinline__ long long floor_sum(long long n, long long x, long long y) {
-  long long m = kKeyBlock, sum = 0;
+// sum_{k < n} floor((x k + y) / 128): after taking out whole parts, the lattice
+// points under the line are counted along the other axis. x n and y are at most
+// twice the longest sequence, so only the sum needs 64 bits.
+__device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t x, uint32_t y) {
+  uint32_t m = kKeyBlock;
+  long long sum = 0;
   while (n > 0) {
     if (x >= m) {
-      sum += n * (n - 1) / 2 * (x / m);
-      x %= m;
+      const uint32_t q = x / m;
+      sum += static_cast<long long>(n) * (n - 1) / 2 * q;
+      x -= q * m;
     }
     if (y >= m) {
-      sum += n * (y / m);
-      y %= m;
+      const uint32_t q = y / m;
+      sum += static_cast<long long>(n) * q;
+      y -= q * m;
     }
-    const long long top = x * n + y;
+    const uint32_t top = x * n + y;
     if (top < m) break;
     n = top / m;
-    y = top % m;
-    const long long t = m;
+    y = top - n * m;
+    const uint32_t t = m;
     m = x;
     x = t;
   }
   return sum;
 }
 
-// Tiles of a sequence: an item is two query tiles, 2 T tokens.
+// A sequence's tiles: an item is two query tiles, 2 T tokens (the last may be
+// one). A block of an item weighs as many units as it has tiles: two tiles'
+// products bound a block, one tile's are about as fast as its keys arrive, in
+// half the time.
 struct TileMath {
-  int item;  // tokens per item
+  int T;
   int causal;
-  __device__ __forceinline__ int blocks(const SeqInfo& s, int k) const {
-    return blocks(s.m, s.n, min((k + 1) * item, s.m) - 1);
-  }
-  __device__ __forceinline__ int items(const SeqInfo& s) const { return (s.m + item - 1) / item; }
+  __device__ __forceinline__ int items(const SeqInfo& s) const { return (s.m + 2 * T - 1) / (2 * T); }
+  __device__ __forceinline__ int weight(const SeqInfo& s, int k) const { return k * 2 * T + T < s.m ? 2 : 1; }
   // Keys that token i sees.
   __device__ __forceinline__ int seen(int m, int n, int i) const {
     return causal ? max(0, min(n, n - m + i + 1)) : n;
   }
   // Blocks that tokens up to i of the chunk walk.
   __device__ __forceinline__ int blocks(int m, int n, int i) const { return seq_blocks(seen(m, n, i)); }
-  // Blocks of items 0 .. k - 1 (k <= items).
-  __device__ __forceinline__ long long before(const SeqInfo& s, int k) const {
-    if (!causal) return static_cast<long long>(k) * seq_blocks(s.n);
-    if (k == 0) return 0;
-    long long sum = 0;
-    if (k == items(s)) {  // the last item may hold fewer tokens
-      sum = seq_blocks(s.n);
-      --k;
-    }
-    // Item i's last token sees x(i) = n - m + (i + 1) item keys; where x <= 0
-    // it walks the one block that writes its zeros.
-    const long long c = static_cast<long long>(s.n) - s.m;
-    const long long none = c < 0 ? min(static_cast<long long>(k), -c / item) : 0;
-    return sum + none + floor_sum(k - none, item, c + (none + 1) * item + kKeyBlock - 1);
+  __device__ __forceinline__ int blocks(const SeqInfo& s, int k) const {
+    return blocks(s.m, s.n, min((k + 1) * 2 * T, s.m) - 1);
   }
+  // Units of items 0 .. k - 1 (k <= items).
+  __device__ __forceinline__ long long before(const SeqInfo& s, int k) const {
+    long long sum = 0;
+    if (k > 0 && k == items(s)) {  // the last item may hold fewer tokens
+      --k;
+      sum = static_cast<long long>(seq_blocks(s.n)) * weight(s, k);
+    }
+    if (!causal) return sum + 2ll * k * seq_blocks(s.n);
+    // Item i's last token sees x(i) = n - m + (i + 1) 2 T keys; where x <= 0 it
+    // walks the one block that writes its zeros.
+    const int item = 2 * T, c = s.n - s.m;
+    const int none = c < 0 ? min(k, -c / item) : 0;
+    return sum + 2ll * none + 2 * floor_sum(k - none, item, c + (none + 1) * item + kKeyBlock - 1);
+  }
+};
+
+// Where a segment's parts differ by its tiles. Two tiles: each works on the blocks
+// that its rows see. One tile: "dual" from two blocks on, both sides take blocks
+// in turn for the one tile; else side 0 works alone.
+struct Shape {
+  bool two, dual;
 };
 
 }  // namespace
@@ -127,7 +148,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
                       const __grid_constant__ CUtensorMap tm_v, const PagedAttend a) {
   using C = ManyCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ ManyBarriers<C::KST, C::VST> bar;
+  __shared__ ManyBarriers<C::QST, C::KST, C::VST> bar;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sK = smem + C::OFF_K;
@@ -138,8 +159,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
   constexpr int kProducer = C::EPI_WARPS, kIssuer = C::EPI_WARPS + 1;
 
   if (threadIdx.x == 0) {
-    mbar_init(&bar.q_full, 1);
-    mbar_init(&bar.q_empty, 2);
+    for (int s = 0; s < C::QST; ++s) { mbar_init(&bar.q_full[s], 1); mbar_init(&bar.q_empty[s], 2); }
     for (int s = 0; s < C::KST; ++s) { mbar_init(&bar.k_full[s], 1); mbar_init(&bar.k_empty[s], 2); }
     for (int s = 0; s < C::VST; ++s) { mbar_init(&bar.v_full[s], 1); mbar_init(&bar.v_empty[s], 2); }
     for (int t = 0; t < 2; ++t) {
@@ -152,6 +172,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
       mbar_init(&bar.s_read[t], 8);
       mbar_init(&bar.pv_done[t], 1);
       mbar_init(&bar.drain[t], 1);
+      for (int s = 0; s < 4; ++s) mbar_init(&bar.fin[t][s], 1);
     }
     mbar_init(&bar.stored, C::EPI_WARPS);
     mbar_init(&bar.counted, 1);
@@ -165,7 +186,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
   }
   const int G = a.Hq / a.Hkv;
   const int T = 128 / G;  // tokens per tile
-  const TileMath math{2 * T, a.causal};
+  const TileMath math{T, a.causal};
   grid_dep_launch();
   grid_dep_wait();
   plan_run<C::THREADS>(a, &bar.run, [&](const SeqInfo& s) { return math.before(s, math.items(s)); });
@@ -174,9 +195,13 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = bar.tmem_base;
 
-  // Tile t of a segment works on blocks [j0, end): none where it has no tokens
-  // or its rows see none of them.
-  auto tile_end = [&](const Segment& seg, int t) {
+  auto shape = [&](const Segment& seg) {
+    const bool two = seg.tile * 2 * T + T < seg.m;
+    return Shape{two, !two && seg.j1 - seg.j0 > 1};
+  };
+  // Side t of a segment that is not dual works on blocks [j0, end): none where
+  // its tile has no tokens or its rows see none of them.
+  auto side_end = [&](const Segment& seg, int t) {
     const int i0 = seg.tile * 2 * T + t * T;
     if (i0 >= seg.m) return seg.j0;
     return max(seg.j0, min(seg.j1, math.blocks(seg.m, seg.n, min(i0 + T, seg.m) - 1)));
@@ -190,25 +215,26 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
       tma_prefetch_desc(&tm_v);
     }
     const int rb = min(1 << a.page_shift, kKeyBlock);  // keys per box
-    uint32_t rst = 0, rph = 0, qph = 0;
+    uint32_t rst = 0, rph = 0, qst = 0, qph = 0, q_loads = 0;
     uint32_t st[2] = {0, 0}, ph[2] = {0, 0}, loads[2] = {0, 0};
-    int q_last = -1;
     bool ok = true;
     RunWalker<TileMath> walk(a, math, bar.run, lane);
     const Segment& seg = walk.seg;
-    for (bool more = bar.run.count > 0; ok && more; more = ok && walk.next()) {
+    for (; ok && walk.alive; walk.next()) {
       if (!(ok = seg_publish(bar.ring, rst, rph, seg, lane, abort_flag, ws, 400))) break;
-      if (!(ok = warp_wait(&bar.q_empty, qph ^ 1, abort_flag, ws, 401))) break;
-      if (lane == 0) {
-        const int i0 = seg.tile * 2 * T, ntiles = i0 + T < seg.m ? 2 : 1;
-        mbar_arrive_expect_tx(&bar.q_full, ntiles * T * G * 128 * C::CH);
-        for (int t = 0; t < ntiles; ++t)
+      const int i0 = seg.tile * 2 * T, ntiles = i0 + T < seg.m ? 2 : 1;
+      for (int t = 0; ok && t < ntiles; ++t) {
+        if (!(ok = warp_wait(&bar.q_empty[qst], qph ^ 1, abort_flag, ws, 401))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bar.q_full[qst], T * G * 128 * C::CH);
           for (int c = 0; c < C::CH; ++c)
-            tma_load_3d(sQ + t * C::TILE_BYTES + c * C::BOX_BYTES, &tm_q, &bar.q_full, c * 64, seg.head * G,
+            tma_load_3d(sQ + qst * C::TILE_BYTES + c * C::BOX_BYTES, &tm_q, &bar.q_full[qst], c * 64, seg.head * G,
                         seg.start + i0 + t * T);
+        }
+        __syncwarp();
+        ++q_loads;
+        if (++qst == C::QST) { qst = 0; qph ^= 1; }
       }
-      q_last = static_cast<int>(qph);
-      qph ^= 1;
       for (int j = seg.j0; ok && j < seg.j1; ++j) {
         const int keys = min(kKeyBlock, seg.n - j * kKeyBlock);
         const int boxes = (keys + rb - 1) / rb;  // 0 for a sequence without keys
@@ -241,146 +267,187 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
           mbar_wait(kv ? &bar.v_full[idx % slots] : &bar.k_full[idx % slots], (idx / slots) & 1, no_abort, nullptr, 0);
         }
       }
-      if (q_last >= 0) mbar_wait(&bar.q_full, q_last, no_abort, nullptr, 0);
+      for (uint32_t x = 0; x < C::QST && x < q_loads; ++x) {
+        const uint32_t idx = q_loads - 1 - x;
+        mbar_wait(&bar.q_full[idx % C::QST], (idx / C::QST) & 1, no_abort, nullptr, 0);
+      }
     }
   } else if (warp >= kIssuer) {
-    // ------------------------------------------------------- issuer of tile t
+    // ------------------------------------------------------- issuer of side t
     // Both issuers wait for every load and give an arrival on every "empty"
-    // barrier, whether or not their tile works on the block. Lane 0 issues; the
-    // whole warp walks along to zero the rows of V past a text's end.
+    // barrier (each sees every phase), whether or not their side works on the
+    // block. One thread each: a tile's chain of S, weights and PV sets the pace,
+    // and every warp-wide step in it costs (4450 cycles a block against 4200).
     const int t = warp - kIssuer;
-    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
-    constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, false, true);
-    const uint64_t d_q = smem_desc_sw128(smem_u32(sQ), 16, 1024) + ((t * C::TILE_BYTES) >> 4);
-    const uint64_t d_k = smem_desc_sw128(smem_u32(sK), 16, 1024);
-    const uint64_t d_v = smem_desc_sw128(smem_u32(sV), C::BOX_BYTES, 1024);  // MN-major view of V
-    constexpr uint64_t kTile = C::TILE_BYTES >> 4;
-    const uint32_t tm_s = tmem + C::TM_S + t * 128;
-    const uint32_t tm_o = tmem + C::TM_O + t * D;
-    const uint32_t tm_p = C::SEP_P ? tmem + C::TM_P + t * 64 : tm_s;
-    constexpr int kPHalf = C::SEP_P ? 32 : 64;
-    uint32_t kst = 0, kph = 0, vst = 0, vph = 0, qph = 0, pph[2] = {0, 0}, oph = 0, srph = 0, rst = 0, rph = 0;
-    bool s_pending = false;  // SEP_P: an S was issued whose copy-out has not been awaited
-    bool ok = true;
-    while (ok) {
-      Segment seg;
-      if (!(ok = seg_read<true>(bar.ring, rst, rph, &seg, abort_flag, ws, 410))) break;
-      __syncwarp();
-      seg_release(bar.ring, rst, rph, lane == 0);
-      if (seg.j1 < 0) break;
-      const int end = tile_end(seg, t);
-      if (!(ok = warp_wait(&bar.q_full, qph, abort_flag, ws, 411))) break;
-      qph ^= 1;
-      auto take_k = [&](int j) -> bool {
-        if (!warp_wait(&bar.k_full[kst], kph, abort_flag, ws, 412)) return false;
-        if (j < end) {
-          if (C::SEP_P && s_pending) {  // the epilogue must have copied the previous S out
-            if (!warp_wait(&bar.s_read[t], srph, abort_flag, ws, 413)) return false;
-            srph ^= 1;
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, false, true);
+      const uint64_t d_q = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t d_k = smem_desc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t d_v = smem_desc_sw128(smem_u32(sV), C::BOX_BYTES, 1024);  // MN-major view of V
+      constexpr uint64_t kTile = C::TILE_BYTES >> 4;
+      const uint32_t tm_o = tmem + C::TM_O + t * D;
+      constexpr int kPHalf = C::SEP_P ? 32 : 64;
+      uint32_t kst = 0, kph = 0, vst = 0, vph = 0, qst = 0, qph = 0, oph = 0, rst = 0, rph = 0, segs = 0;
+      // Per side e (bit e): parity of the blocks so far, and whether there were any.
+      // Both issuers keep both sides' bits, since dual segments swap the issuer.
+      uint32_t odd = 0, any = 0;
+      bool was_two = false;  // the previous segment had two tiles
+      bool ok = true;
+      while (ok) {
+        Segment seg;
+        if (!(ok = seg_read<false>(bar.ring, rst, rph, &seg, abort_flag, ws, 410))) break;
+        seg_release(bar.ring, rst, rph, true);
+        if (seg.j1 < 0) break;
+        const Shape sh = shape(seg);
+        const int end = side_end(seg, t);
+        const int len = seg.j1 - seg.j0;
+        // Side 1's regions change issuers between a segment of two tiles and a dual
+        // one: the other issuer's products must have completed. (No issuer gets
+        // four segments ahead of the other: the K ring is shorter.)
+        if (segs > 0 && (t == 0 ? was_two && !sh.two : sh.two && !was_two) &&
+            !(ok = mbar_wait(&bar.fin[1 - t][(segs - 1) & 3], ((segs - 1) >> 2) & 1, abort_flag, ws, 417)))
+          break;
+        uint64_t q_tile = 0;  // this side's query tile (dual: the only one)
+        uint64_t* q_free = nullptr;
+        for (int x = 0; x <= (sh.two ? 1 : 0); ++x) {
+          if (!(ok = mbar_wait(&bar.q_full[qst], qph, abort_flag, ws, 411))) break;
+          if (x == t) {
+            q_tile = d_q + qst * kTile;
+            q_free = &bar.q_empty[qst];
+          } else {
+            mbar_arrive(&bar.q_empty[qst]);
           }
-          s_pending = true;
-          tc_fence_after();
-          if (lane == 0) {
+          if (++qst == C::QST) { qst = 0; qph ^= 1; }
+        }
+        if (!ok) break;
+        uint32_t fresh = 0;  // 1 once the segment's O holds a product
+        // The side that block j works on here, or -1.
+        auto side_of = [&](int j) { return sh.dual ? (t == 0 ? (j - seg.j0) & 1 : -1) : (j < end ? t : -1); };
+        auto take_k = [&](int j) -> bool {
+          if (!mbar_wait(&bar.k_full[kst], kph, abort_flag, ws, 412)) return false;
+          const int e = side_of(j);
+          if (e >= 0) {
+            // SEP_P: the epilogue must have copied the side's previous S out.
+            if (C::SEP_P && (any >> e & 1) && !mbar_wait(&bar.s_read[e], (odd >> e & 1) ^ 1, abort_flag, ws, 413)) return false;
+            odd ^= 1u << e;
+            any |= 1u << e;
+            tc_fence_after();
+            const uint32_t tm_s = tmem + C::TM_S + e * 128;
+            const uint64_t b0 = d_k + kst * kTile;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint64_t off = ((kk >> 2) * C::BOX_BYTES + (kk & 3) * 32) >> 4;
-              mma_ss(tm_s, d_q + off, d_k + kst * kTile + off, idesc_s, kk > 0 ? 1u : 0u);
+              mma_ss(tm_s, q_tile + off, b0 + off, idesc_s, kk > 0 ? 1u : 0u);
             }
-            mma_commit(&bar.s_full[t]);
+            mma_commit(&bar.s_full[e]);
           }
-        }
-        if (lane == 0) {
-          if (j + 1 == seg.j1) mma_commit(&bar.q_empty);
+          if (j + 1 == seg.j1 && q_free != nullptr) mma_commit(q_free);
           mma_commit(&bar.k_empty[kst]);
-        }
-        __syncwarp();
-        if (++kst == C::KST) { kst = 0; kph ^= 1; }
-        return true;
-      };
-      auto take_v = [&](int j) -> bool {
-        if (!warp_wait(&bar.v_full[vst], vph, abort_flag, ws, 414)) return false;
-        if (j < end) {
-          // The products take keys in sixteens: rows of V past the text's end in
-          // the last sixteen are zeroed (their weights are 0, and 0 * NaN must
-          // not be). Both issuers write the same zeros.
-          const int keys = min(kKeyBlock, seg.n - j * kKeyBlock);
-          const int steps = max(1, (keys + 15) / 16);
-          if (keys < steps * 16) {
-            uint4* v = reinterpret_cast<uint4*>(sV + vst * C::TILE_BYTES);
-            for (int i = lane; i < (steps * 16 - keys) * 8; i += 32)
-              for (int c = 0; c < C::CH; ++c) v[(c * C::BOX_BYTES + keys * 128) / 16 + i] = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (!warp_wait(&bar.p_full[2 * t + h], pph[h], abort_flag, ws, 415)) return false;
-            pph[h] ^= 1;
-            if (j == seg.j0 && h == 0) {
-              if (!warp_wait(&bar.o_empty[t], oph ^ 1, abort_flag, ws, 416)) return false;
-              oph ^= 1;
+          if (++kst == C::KST) { kst = 0; kph ^= 1; }
+          return true;
+        };
+        uint32_t podd = odd;  // parity of the side's blocks before the one whose P is taken next
+        auto take_v = [&](int j) -> bool {
+          if (!mbar_wait(&bar.v_full[vst], vph, abort_flag, ws, 414)) return false;
+          const int e = side_of(j);
+          if (e >= 0) {
+            // The products take keys in sixteens: rows of V past the text's end in
+            // the last sixteen are zeroed (their weights are 0, and 0 * NaN must
+            // not be). Both issuers write the same zeros.
+            const int keys = min(kKeyBlock, seg.n - j * kKeyBlock);
+            const int steps = max(1, (keys + 15) / 16);
+            if (keys < steps * 16) {
+              uint4* v = reinterpret_cast<uint4*>(sV + vst * C::TILE_BYTES);
+              for (int i = 0; i < (steps * 16 - keys) * 8; ++i)
+                for (int c = 0; c < C::CH; ++c) v[(c * C::BOX_BYTES + keys * 128) / 16 + i] = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
             }
-            tc_fence_after();
-            if (lane == 0) {
+            const uint32_t tm_p = tmem + (C::SEP_P ? C::TM_P + e * 64 : C::TM_S + e * 128);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (!mbar_wait(&bar.p_full[2 * e + h], podd >> e & 1, abort_flag, ws, 415)) return false;
+              if (fresh == 0 && h == 0) {
+                if (!mbar_wait(&bar.o_empty[t], oph ^ 1, abort_flag, ws, 416)) return false;
+                oph ^= 1;
+              }
+              tc_fence_after();
               const uint64_t b0 = d_v + vst * kTile + ((h * 64 * 128) >> 4);
+              if (steps == 8) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                if (4 * h + kk < steps)
-                  mma_ts(tm_o, tm_p + h * kPHalf + kk * 8, b0 + ((kk * 2048) >> 4), idesc_o,
-                         (j > seg.j0 || h > 0 || kk > 0) ? 1u : 0u);
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_ts(tm_o, tm_p + h * kPHalf + kk * 8, b0 + ((kk * 2048) >> 4), idesc_o, (h > 0 || kk > 0) ? 1u : fresh);
+              } else {
+                for (int kk = 0; kk < min(4, steps - 4 * h); ++kk)
+                  mma_ts(tm_o, tm_p + h * kPHalf + kk * 8, b0 + ((kk * 2048) >> 4), idesc_o, (h > 0 || kk > 0) ? 1u : fresh);
+              }
             }
+            podd ^= 1u << e;
+            fresh = 1;
           }
-        }
-        if (lane == 0) {
           mma_commit(&bar.v_empty[vst]);
-          if (C::SEP_P && j < end) mma_commit(&bar.pv_done[t]);
+          if (C::SEP_P && e >= 0) mma_commit(&bar.pv_done[e]);
+          if (++vst == C::VST) { vst = 0; vph ^= 1; }
+          return true;
+        };
+        // S(j + ahead) goes before PV(j) where its region is free of P(j): P has a
+        // region of its own (d = 64), or the next block is the other side's
+        // (dual). Otherwise S(j + 1) overwrites P(j) and follows PV(j).
+        const int ahead = (C::SEP_P || sh.dual) ? 1 : 0;
+        if (!(ok = take_k(seg.j0))) break;
+        for (int j = seg.j0; ok && j < seg.j1; ++j) {
+          if (ahead && j + 1 < seg.j1 && !(ok = take_k(j + 1))) break;
+          if (!(ok = take_v(j))) break;
+          if (!ahead && j + 1 < seg.j1 && !(ok = take_k(j + 1))) break;
         }
-        __syncwarp();
-        if (++vst == C::VST) { vst = 0; vph ^= 1; }
-        return true;
-      };
-      if (!(ok = take_k(seg.j0))) break;
-      for (int j = seg.j0; ok && j < seg.j1; ++j) {
-        // S(j + 1) goes first where P has its own region; otherwise it
-        // overwrites P(j) and follows PV(j).
-        if (C::SEP_P && j + 1 < seg.j1 && !(ok = take_k(j + 1))) break;
-        if (!(ok = take_v(j))) break;
-        if (!C::SEP_P && j + 1 < seg.j1 && !(ok = take_k(j + 1))) break;
+        if (!ok) break;
+        if (fresh) mma_commit(&bar.o_full[t]);
+        mma_commit(&bar.fin[t][segs & 3]);
+        // The other side's blocks, or (dual, t = 1) both sides'.
+        const int theirs = sh.dual ? (t == 1 ? len / 2 : 0) : side_end(seg, 1 - t) - seg.j0;
+        odd ^= static_cast<uint32_t>(theirs & 1) << (sh.dual ? 1 : 1 - t);
+        if (theirs > 0) any |= 1u << (sh.dual ? 1 : 1 - t);
+        if (sh.dual && t == 1) {
+          odd ^= static_cast<uint32_t>((len + 1) / 2 & 1);
+          any |= 1u;
+        }
+        was_two = sh.two;
+        ++segs;
       }
-      if (!ok) break;
-      if (lane == 0 && seg.j0 < end) mma_commit(&bar.o_full[t]);
-      __syncwarp();
-    }
-    if (lane == 0) {
       int never = 0;
       mma_commit(&bar.drain[t]);
       mbar_wait(&bar.drain[t], 0, &never, ws, 419);
     }
-    __syncwarp();
   } else {
     // ------------------------------------------------------------- epilogue
-    const int t = warp >> 3;                       // query tile of this warp
+    const int t = warp >> 3;                       // side of this warp
     const int h = (warp >> 2) & 1;                 // its half (64 keys) of each block
-    const int r = ((warp & 3) << 5) + lane;        // row within the tile = TMEM lane
-    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) << 5) << 16;
-    const uint32_t tS = tmem + lane_off + C::TM_S + t * 128 + h * 64;
-    const uint32_t tP = C::SEP_P ? tmem + lane_off + C::TM_P + t * 64 + h * 32 : tS;
-    const uint32_t tO = tmem + lane_off + C::TM_O + t * D + h * (D / 2);
+    const int r = threadIdx.x & 127;               // row within the tile = TMEM lane
+    const uint32_t quad = tmem + (static_cast<uint32_t>(r & 96) << 16);
+    const uint32_t tS = quad + C::TM_S + t * 128 + h * 64;
     constexpr float scale_l2e = Scale<D>::value * kLog2e;
-    const int ri = r / G, rg = r - ri * G;         // the row's token and head within the tile
-    uint32_t sph = 0, oph = 0, turn_ph = 0, pvph = 0, rst = 0, rph = 0, parts = 0;
-    bool pv_pending = false;  // SEP_P: a P was written whose PV has not been awaited
-    bool turned = false;      // a block was shared with the other tile before
+    uint32_t rst = 0, rph = 0;
+    // Bits in one register (the passes leave few): parities of the waits for S, O,
+    // the turn, PV and parts; kPending: a P was written whose PV has not been
+    // awaited (SEP_P); kTurned: a block was shared with the other tile before.
+    enum : uint32_t { kS = 1, kO = 2, kTurn = 4, kPv = 8, kParts = 16, kPending = 32, kTurned = 64 };
+    uint32_t bits = 0;
     bool ok = true;
     while (ok) {
       Segment seg;
       if (!(ok = seg_read<true>(bar.ring, rst, rph, &seg, abort_flag, ws, 420))) break;
       if (seg.j1 < 0) break;
-      const int i0 = seg.tile * 2 * T + t * T;
-      const int seg_j0 = seg.j0, end = tile_end(seg, t), other_end = tile_end(seg, 1 - t);
-      const int i = i0 + ri;
-      const bool row_ok = ri < T && i < seg.m;
-      const int seen = math.seen(seg.m, seg.n, i);
+      const Shape sh = shape(seg);
+      const int i0 = seg.tile * 2 * T + (sh.dual ? 0 : t * T);
+      // This side's blocks: from `j` on, every `step`-th, below `end`. Blocks below
+      // `joint_end` are shared with the other tile.
+      const int step = sh.dual ? 2 : 1;
+      const int end = sh.dual ? seg.j1 : side_end(seg, t);
+      int j = sh.dual ? seg.j0 + t : seg.j0;
+      const int joint_end = (!C::SEP_P && sh.two) ? min(end, side_end(seg, 1 - t)) : 0;
+      const int ri = r / G;  // the row's token within the tile
+      const bool row_ok = ri < T && i0 + ri < seg.m;
+      const int seen = math.seen(seg.m, seg.n, i0 + ri);
       const float neg_log2n = -__log2f(static_cast<float>(max(seen, 1)));
       const int clear = math.seen(seg.m, seg.n, i0);  // keys that every row of the tile sees
       // Warps whose rows are all past the tile's last leave S and P alone
@@ -389,16 +456,18 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
       // One pass over key block j; the rows' masks only in MASKED passes.
       auto pass = [&](const int j, auto masked) -> bool {
         constexpr bool MASKED = decltype(masked)::value;
-        if (!warp_wait(&bar.s_full[t], sph, abort_flag, ws, 421)) return false;
-        sph ^= 1;
+        if (!warp_wait(&bar.s_full[t], (bits & kS) != 0, abort_flag, ws, 421)) return false;
+        bits ^= kS;
         // d = 128: the tiles take turns over the blocks that both work on (tile 1
         // follows tile 0 on each, tile 0 follows tile 1's previous one).
-        const bool joint = !C::SEP_P && j < end && j < other_end;
-        if (joint && (t == 1 || turned)) {
-          if (!warp_wait(&bar.epi_done[1 - t], turn_ph, abort_flag, ws, 422)) return false;
-          turn_ph ^= 1;
+        const bool joint = !C::SEP_P && j < joint_end;
+        if (joint) {
+          if (t == 1 || (bits & kTurned)) {
+            if (!warp_wait(&bar.epi_done[1 - t], (bits & kTurn) != 0, abort_flag, ws, 422)) return false;
+            bits ^= kTurn;
+          }
+          bits |= kTurned;
         }
-        turned |= joint;
         tc_fence_after();
         if (!idle) {
 #pragma unroll
@@ -417,22 +486,22 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
             for (int e = 0; e < 16; ++e)
               pk[e] = pack_bf16x2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
             // SEP_P: the P region is free once the tile's previous PV completed.
-            if (C::SEP_P && c == 0 && pv_pending) {
-              if (!warp_wait(&bar.pv_done[t], pvph, abort_flag, ws, 423)) return false;
-              pvph ^= 1;
+            if (C::SEP_P && c == 0 && (bits & kPending)) {
+              if (!warp_wait(&bar.pv_done[t], (bits & kPv) != 0, abort_flag, ws, 423)) return false;
+              bits ^= kPv;
               tc_fence_after();
             }
-            tmem_st16(tP + 16 * c, pk);
+            tmem_st16((C::SEP_P ? quad + C::TM_P + t * 64 + h * 32 : tS) + 16 * c, pk);
           }
           tmem_st_wait();
         } else if (C::SEP_P) {
           if (lane == 0) mbar_arrive(&bar.s_read[t]);
-          if (pv_pending) {
-            if (!warp_wait(&bar.pv_done[t], pvph, abort_flag, ws, 423)) return false;
-            pvph ^= 1;
+          if (bits & kPending) {
+            if (!warp_wait(&bar.pv_done[t], (bits & kPv) != 0, abort_flag, ws, 423)) return false;
+            bits ^= kPv;
           }
         }
-        pv_pending = true;
+        if (C::SEP_P) bits |= kPending;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -441,87 +510,88 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         }
         return true;
       };
-      int j = seg_j0;
       const int plain = min(end, clear / kKeyBlock);  // blocks that every row sees whole
-      for (; ok && j < plain; ++j) ok = pass(j, std::false_type{});
-      for (; ok && j < end; ++j) ok = pass(j, std::true_type{});
+      for (; ok && j < plain; j += step) ok = pass(j, std::false_type{});
+      for (; ok && j < end; j += step) ok = pass(j, std::true_type{});
       if (!ok) break;
 
       // The segment again, from the ring (its slot is released only below, so
       // that the passes need not keep it in registers).
       seg = seg_peek(bar.ring, rst);
+      const Shape out = shape(seg);
+      const bool holds = out.dual ? t == 0 : seg.j0 < side_end(seg, t);  // this side's O holds a sum
       const bool whole = seg.j0 == 0 && seg.j1 == seg.blocks;
-      const int token = seg.tile * 2 * T + t * T + ri;
-      const bool writes = ri < T && token < seg.m;
+      const int of = r / G, token = seg.tile * 2 * T + t * T + of;
+      const bool writes = of < T && token < seg.m;
       __nv_bfloat16* dst =
-          a.o + (static_cast<size_t>(seg.start + token) * a.Hq + seg.head * G + rg) * D + h * (D / 2);
+          a.o + (static_cast<size_t>(seg.start + token) * a.Hq + seg.head * G + r - of * G) * D + h * (D / 2);
+      // A part holds [tile][4 columns][row]: the lanes of a warp, which own rows,
+      // write and read 512 bytes in a row.
       constexpr size_t kPart = static_cast<size_t>(256) * D;
-      const size_t mine = static_cast<size_t>(t * 128 + r) * D + h * (D / 2);
+      const size_t mine = static_cast<size_t>(t * 128) * D + (h * (D / 8) * 128 + r) * 4;
       // This warp's D / 2 columns of O, 32 at a time.
-      if (seg.j0 < end) {
-        if (!(ok = warp_wait(&bar.o_full[t], oph, abort_flag, ws, 424))) break;
-        oph ^= 1;
+      if (holds) {
+        if (!(ok = warp_wait(&bar.o_full[t], (bits & kO) != 0, abort_flag, ws, 424))) break;
+        bits ^= kO;
         tc_fence_after();
         float* part = a.parts + (2 * blockIdx.x + (seg.j0 == 0)) * kPart + mine;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
           uint32_t v[32];
-          tmem_ld32(tO + c * 32, v);
+          tmem_ld32(quad + C::TM_O + t * D + h * (D / 2) + c * 32, v);
           if (c == D / 64 - 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.o_empty[t]);
           }
           if (!writes) continue;
-          if (whole) store_row32(dst + c * 32, v, 1.0f);
-          else store_row_f32(part + c * 32, v);
+          if (whole) {
+            store_row32(dst + c * 32, v, 1.0f);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              __stcg(reinterpret_cast<uint4*>(part + (c * 8 + q) * 512),
+                     make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
+          }
         }
       }
       if (!whole) {
-        if (!(ok = last_part(&bar.stored, &bar.counted, &bar.last, seg, ws, warp, lane, parts, abort_flag, 425))) break;
-        parts ^= 1;
+        if (!(ok = last_part(&bar.stored, &bar.counted, &bar.last, seg, ws, warp, lane, (bits & kParts) != 0, abort_flag,
+                             425)))
+          break;
+        bits ^= kParts;
       }
-      if (!whole && bar.last) {
-        // The sum of the tiles' parts. Lanes take four columns each, so a warp
-        // reads SUB rows of a part at once, and it reads RB such rows (all of one
-        // tile) before it adds any. The first part lies in its CTA's second
-        // place, the others in their CTA's first; parts that start past the
-        // tile's last block are not there.
-        constexpr int LPR = D / 4, SUB = 32 / LPR, STEP = C::EPI_WARPS * SUB, RB = 128 / STEP;
-        for (int u = 0; u < 2; ++u) {
-          const int u0 = seg.tile * 2 * T + u * T;
-          if (u0 >= seg.m) break;
-          const int all = math.blocks(seg.m, seg.n, min(u0 + T, seg.m) - 1);
-          const int row0 = warp * SUB + lane / LPR, used = min(T, seg.m - u0) * G;
-          const float* from = a.parts + (2 * seg.first_cta + 1) * kPart + (u * 128 + row0) * D + 4 * (lane % LPR);
-          float4 sum[RB];
+      if (!whole && bar.last && writes) {
+        // The first part lies in its CTA's second place, the others in their
+        // CTA's first. Parts that start past the tile's last block are not there.
+        const int all = math.blocks(seg.m, seg.n, min(token - of + T, seg.m) - 1);
+        int np = 1;
+        while (np <= seg.last_cta - seg.first_cta && part_begin(seg, np, bar.run.per, out.two ? 2 : 1) < all) ++np;
+        const float* from = a.parts + (2 * seg.first_cta + 1) * kPart + mine;
+        for (int c = 0; c < D / 32; ++c, from += 4 * 512) {
+          float4 sum[4];
 #pragma unroll
-          for (int k = 0; k < RB; ++k) sum[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int p = 0; p <= seg.last_cta - seg.first_cta; ++p) {
-            if (p > 0 && p * bar.run.per - seg.lead >= all) break;
-            float4 x[RB];
+          for (int q = 0; q < 4; ++q) sum[q] = __ldcg(reinterpret_cast<const float4*>(from + q * 512));
+#pragma unroll 2
+          for (int p = 1; p < np; ++p) {
+            float4 x[4];
 #pragma unroll
-            for (int k = 0; k < RB; ++k) {
-              x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (row0 + k * STEP < used) x[k] = __ldcg(reinterpret_cast<const float4*>(from + k * STEP * D));
+            for (int q = 0; q < 4; ++q)
+              x[q] = __ldcg(reinterpret_cast<const float4*>(from + (2 * p - 1) * kPart + q * 512));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              sum[q].x += x[q].x;
+              sum[q].y += x[q].y;
+              sum[q].z += x[q].z;
+              sum[q].w += x[q].w;
             }
-#pragma unroll
-            for (int k = 0; k < RB; ++k) {
-              sum[k].x += x[k].x;
-              sum[k].y += x[k].y;
-              sum[k].z += x[k].z;
-              sum[k].w += x[k].w;
-            }
-            from += (p == 0 ? 1 : 2) * kPart;
           }
 #pragma unroll
-          for (int k = 0; k < RB; ++k) {
-            const int row = row0 + k * STEP;
-            if (row < used)
-              *reinterpret_cast<uint2*>(
-                  a.o + (static_cast<size_t>(seg.start + u0 + row / G) * a.Hq + seg.head * G + row % G) * D +
-                  4 * (lane % LPR)) = make_uint2(pack_bf16x2(sum[k].x, sum[k].y), pack_bf16x2(sum[k].z, sum[k].w));
-          }
+          for (int q = 0; q < 2; ++q)
+            *reinterpret_cast<uint4*>(dst + c * 16 + q * 8) =
+                make_uint4(pack_bf16x2(sum[2 * q].x, sum[2 * q].y), pack_bf16x2(sum[2 * q].z, sum[2 * q].w),
+                           pack_bf16x2(sum[2 * q + 1].x, sum[2 * q + 1].y),
+                           pack_bf16x2(sum[2 * q + 1].z, sum[2 * q + 1].w));
         }
       }
       __syncwarp();

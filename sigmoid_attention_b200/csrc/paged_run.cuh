@@ -8,7 +8,11 @@
 // that lies in the run) to the other roles through a ring in shared memory.
 // A tile whose blocks lie in several CTAs is joined by the CTA that stores
 // its part last (last_part).
+// Blocks may weigh 1 or 2 units (a block for one query tile or for two); a block
+// belongs to the CTA in whose run its first unit lies.
 #pragma once
+
+#include <climits>
 
 #include "paged.cuh"
 
@@ -33,33 +37,41 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 struct SeqInfo {
   int start, m, n;
 };
-__device__ __forceinline__ bool seq_info(const PagedAttend& a, int b, SeqInfo* s) {
-  const int start = __ldcg(a.cu + b), end = __ldcg(a.cu + b + 1), n = __ldcg(a.kv + b);
-  const bool ok = start >= 0 && end >= start && end <= a.total && end - start <= a.max_q && n >= 0 &&
-                  n <= a.max_pages << a.page_shift;
-  s->start = start;
-  s->m = ok ? end - start : 0;
-  s->n = n;
+// (as loaded: loads are issued ahead and checked when they are needed)
+struct SeqWords {
+  int start, end, n;
+};
+__device__ __forceinline__ SeqWords seq_load(const PagedAttend& a, int b) {
+  b = min(b, a.B - 1);
+  return SeqWords{__ldcg(a.cu + b), __ldcg(a.cu + b + 1), __ldcg(a.kv + b)};
+}
+__device__ __forceinline__ bool seq_check(const PagedAttend& a, const SeqWords& w, SeqInfo* s) {
+  const bool ok = w.start >= 0 && w.end >= w.start && w.end <= a.total && w.end - w.start <= a.max_q && w.n >= 0 &&
+                  w.n <= a.max_pages << a.page_shift;
+  s->start = w.start;
+  s->m = ok ? w.end - w.start : 0;
+  s->n = w.n;
   return ok;
 }
 
-// x / y and x % y of nonnegative numbers: unit counts nearly always fit 32 bits,
-// where a division takes a fraction of the time.
+// x / y of nonnegative numbers: unit counts nearly always fit 32 bits, where a
+// division takes a fraction of the time.
 __device__ __forceinline__ long long fast_div(long long x, long long y) {
   if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
   return x / y;
 }
 
-// A CTA's run: units [first, first + count), `per` units to a CTA; its first
-// unit is unit `rem` of sequence b.
+// A CTA's run: `count` units from unit blockIdx.x * per of the line on, which is
+// unit `rem` of sequence b.
 struct PlanRun {
-  long long first, count, per, rem;
+  long long rem;
   SeqInfo s;
-  int b;
+  int b, count, per;
 };
 
 // units(s): units of one key/value head of a sequence with new tokens. Runs are
-// at least a.least units long (a run's fixed costs are then worth paying).
+// at least a.least units long (at least a block's weight, so that a tile's CTAs
+// all have a block of it).
 // Ends before the caller's next barrier; every thread of the CTA takes part.
 template <int THREADS, typename Units>
 __device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun* run, Units units) {
@@ -70,7 +82,7 @@ __device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun* run, Uni
   const int b0 = min(a.B, tid * chunk), b1 = min(a.B, b0 + chunk);
   SeqInfo s;  // of the sequence that units_of saw last
   auto units_of = [&](int b, bool report) -> long long {
-    if (!seq_info(a, b, &s)) {
+    if (!seq_check(a, seq_load(a, b), &s)) {
       if (report && blockIdx.x == 0) raise_invalid(a.ws, -(b + 1));
       return 0;
     }
@@ -93,12 +105,15 @@ __device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun* run, Uni
     total += sums[w];
   }
   base += incl - mine;
-  const long long per = max(static_cast<long long>(a.least), fast_div(total + gridDim.x - 1, gridDim.x));
+  long long per = max(static_cast<long long>(a.least), fast_div(total + gridDim.x - 1, gridDim.x));
+  if (per > INT_MAX) {  // beyond any call that could end
+    if (blockIdx.x == 0 && tid == 0) raise_invalid(a.ws, 206);
+    per = total = 0;
+  }
   const long long first = min(total, per * blockIdx.x);
   if (tid == 0) {
-    run->first = first;
-    run->count = min(per, total - first);
-    run->per = per;
+    run->count = static_cast<int>(min(per, total - first));
+    run->per = static_cast<int>(per);
   }
   if (first >= base && first < base + mine) {
     long long rem = first - base;
@@ -114,15 +129,20 @@ __device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun* run, Uni
   }
 }
 
-// Part of one tile's key blocks: blocks [j0, j1) of `blocks`; the tile's
-// first and last blocks lie in CTAs first_cta and last_cta. j1 < 0 ends a run.
+// Part of one tile's key blocks: blocks [j0, j1) of `blocks`. The tile's first
+// and last blocks lie in CTAs first_cta and last_cta, its first unit is unit
+// `lead` of first_cta's run. j1 < 0 ends a run.
 struct Segment {
   int start, m, n, b;
   int head, tile, j0, j1;
-  int blocks, first_cta, last_cta;
-  int lead;  // the first CTA's units before the tile (a part p CTAs on starts at block p * per - lead)
+  int blocks, first_cta, last_cta, lead;
 };
 static_assert(sizeof(Segment) == 48, "three int4");
+
+// The first block of the tile that the p-th CTA after first_cta works on.
+__device__ __forceinline__ int part_begin(const Segment& s, int p, int per, int weight) {
+  return p == 0 ? 0 : static_cast<int>((static_cast<long long>(p) * per - s.lead + weight - 1) / weight);
+}
 
 __device__ __forceinline__ Segment end_segment() {
   Segment s{};
@@ -185,55 +205,52 @@ __device__ __forceinline__ void seg_release(SegRing& r, uint32_t& st, uint32_t& 
 // following 32 entries, the next sequence's first 32 entries) are loaded long
 // before they are needed, so that only the run's first block waits for them.
 //
-// Tiles: items(s), blocks(s, tile) and before(s, k) (the blocks of tiles
-// 0 .. k - 1) of one key/value head of a sequence with new tokens.
+// Tiles: items(s), blocks(s, tile), a block's weight(s, tile) and before(s, k)
+// (the units of tiles 0 .. k - 1) of one key/value head of a sequence with new
+// tokens.
 template <typename Tiles>
 struct RunWalker {
   const PagedAttend& a;
   const Tiles& tiles;
-  const int lane;
-  long long unit, left, per;
+  const int lane, per, count;
+  int pos;     // units of the run up to the current segment's end
+  bool alive;  // there is a current segment
   Segment seg;
   SeqInfo s, next_s;
   int items, next_b;
   int seq_base;
-  SeqInfo seq_cur, seq_ahead;
+  SeqWords seq_cur, seq_ahead;
   const int* row;
   int pages, first, next_first, window, cur, ahead;
 
-  __device__ __forceinline__ SeqInfo load_seq(int b) const {
-    SeqInfo x{0, 0, 0};
-    if (b < a.B) seq_info(a, b, &x);
-    return x;
-  }
-  __device__ __forceinline__ SeqInfo from_lane(const SeqInfo& x, int l) const {
-    return SeqInfo{__shfl_sync(0xffffffffu, x.start, l), __shfl_sync(0xffffffffu, x.m, l),
-                   __shfl_sync(0xffffffffu, x.n, l)};
-  }
   // Find the next sequence after b with new tokens (a.B: none) and start the
   // load of its first page numbers.
   __device__ __forceinline__ void look_ahead(int b) {
     for (;;) {
       const int from = b + 1 - seq_base;  // 1 .. 32
-      unsigned found = __ballot_sync(0xffffffffu, seq_cur.m > 0);
+      SeqInfo x;
+      seq_check(a, seq_cur, &x);
+      unsigned found = __ballot_sync(0xffffffffu, x.m > 0 && seq_base + lane < a.B);
       found = from < 32 ? found >> from << from : 0u;
       if (found) {
-        next_b = seq_base + __ffs(found) - 1;
-        next_s = from_lane(seq_cur, next_b - seq_base);
+        const int l = __ffs(found) - 1;
+        next_b = seq_base + l;
+        next_s = SeqInfo{__shfl_sync(0xffffffffu, x.start, l), __shfl_sync(0xffffffffu, x.m, l),
+                         __shfl_sync(0xffffffffu, x.n, l)};
         next_first = entry(a.table + static_cast<size_t>(next_b) * a.max_pages, pages_of(next_s.n), 0);
         return;
       }
       seq_base += 32;
       if (seq_base >= a.B) break;
       seq_cur = seq_ahead;
-      seq_ahead = load_seq(seq_base + 32 + lane);
+      seq_ahead = seq_load(a, seq_base + 32 + lane);
       b = seq_base - 1;
     }
     next_b = a.B;
   }
   __device__ __forceinline__ int pages_of(int n) const { return (n + (1 << a.page_shift) - 1) >> a.page_shift; }
-  __device__ __forceinline__ int entry(const int* r, int count, int i) const {
-    return i + lane < count ? __ldcg(r + i + lane) : -1;
+  __device__ __forceinline__ int entry(const int* r, int limit, int i) const {
+    return i + lane < limit ? __ldcg(r + i + lane) : -1;
   }
   __device__ __forceinline__ void enter() {
     seg.start = s.start;
@@ -245,53 +262,64 @@ struct RunWalker {
   }
 
   __device__ __forceinline__ RunWalker(const PagedAttend& args, const Tiles& t, const PlanRun& run, int ln)
-      : a(args), tiles(t), lane(ln), unit(run.first), left(run.count), per(run.per) {
-    if (left <= 0) return;
+      : a(args), tiles(t), lane(ln), per(run.per), count(run.count), pos(0), alive(run.count > 0) {
+    if (!alive) return;
     s = run.s;
     seg = Segment{};
     seg.b = run.b;
     enter();
     first = entry(row, pages, 0);
     seq_base = seg.b;
-    seq_cur = load_seq(seq_base + lane);
-    seq_ahead = load_seq(seq_base + 32 + lane);
+    seq_cur = seq_load(a, seq_base + lane);
+    seq_ahead = seq_load(a, seq_base + 32 + lane);
+    next_b = -1;  // looked for when the run's first loads are on their way
     const long long each = tiles.before(s, items);
     seg.head = static_cast<int>(fast_div(run.rem, each));
     const long long rem = run.rem - seg.head * each;
-    int lo = 0, hi = items - 1;  // the last tile with before(tile) <= rem
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (tiles.before(s, mid) <= rem) lo = mid; else hi = mid - 1;
+    // The last tile with before(tile) <= rem, 32 candidates at a time.
+    for (int width = items; width > 1;) {
+      const int step = (width + 31) / 32;
+      const unsigned below =
+          __ballot_sync(0xffffffffu, lane * step < width && tiles.before(s, seg.tile + lane * step) <= rem);
+      const int l = 31 - __clz(below);
+      seg.tile += l * step;
+      width = min(step, width - l * step);
     }
-    seg.tile = lo;
-    seg.j0 = static_cast<int>(rem - tiles.before(s, lo));
-    seg.blocks = tiles.blocks(s, lo);
-    open();
-    next_b = -1;  // looked for when the run's first loads are on their way
+    seg.blocks = tiles.blocks(s, seg.tile);
+    const int weight = tiles.weight(s, seg.tile), off = static_cast<int>(rem - tiles.before(s, seg.tile));
+    seg.j0 = (off + weight - 1) / weight;
+    pos = seg.j0 * weight - off;
+    if (seg.j0 == seg.blocks) alive = step_tile();  // the run starts inside the tile's last block
+    else open();
   }
 
-  // The segment that starts at seg.j0 (left > 0).
+  // The segment that starts at seg.j0, unit `pos` of the run. A tile that began
+  // before it began in the run (only a run's first can); one that does not end
+  // in it is its last.
   __device__ __forceinline__ void open() {
-    const int len = static_cast<int>(min(left, static_cast<long long>(seg.blocks - seg.j0)));
-    const long long tile_unit = unit - seg.j0;  // the tile's first unit
+    const int me = blockIdx.x, weight = tiles.weight(s, seg.tile);
+    const int len = min((count - pos + weight - 1) / weight, seg.blocks - seg.j0);
+    const int begin = pos - seg.j0 * weight;  // where the tile begins, counted from the run's first unit
     seg.j1 = seg.j0 + len;
-    const long long me = blockIdx.x;
-    const bool here = tile_unit >= me * per && tile_unit + seg.blocks <= (me + 1) * per;  // the tile lies in this run
-    seg.first_cta = here ? static_cast<int>(me) : static_cast<int>(fast_div(tile_unit, per));
-    seg.last_cta = here ? static_cast<int>(me) : static_cast<int>(fast_div(tile_unit + seg.blocks - 1, per));
-    seg.lead = static_cast<int>(tile_unit - seg.first_cta * per);
-    unit += len;
-    left -= len;
+    seg.first_cta = me;
+    seg.lead = begin;
+    if (begin < 0) {
+      const int back = (per - 1 - begin) / per;
+      seg.first_cta = me - back;
+      seg.lead = back * per + begin;
+    }
+    seg.last_cta = seg.j1 == seg.blocks ? me : me + (begin + (seg.blocks - 1) * weight) / per;
+    pos += len * weight;
     window = ((seg.j0 * kKeyBlock) >> a.page_shift) & ~31;
     cur = window == 0 ? first : entry(row, pages, window);
     ahead = entry(row, pages, window + 32);
   }
 
-  // On to the run's next segment; false at its end.
-  __device__ __forceinline__ bool next() {
-    if (left <= 0) return false;
-    if (next_b < 0) look_ahead(seg.b);
+  // On to the next tile; false at the run's end.
+  __device__ __forceinline__ bool step_tile() {
+    if (pos >= count) return false;
     seg.j0 = 0;
+    if (next_b < 0) look_ahead(seg.b);
     if (++seg.tile == items) {
       seg.tile = 0;
       if (++seg.head == a.Hkv) {  // the next sequence
@@ -308,6 +336,7 @@ struct RunWalker {
     open();
     return true;
   }
+  __device__ __forceinline__ void next() { alive = step_tile(); }
 
   // Where box `box` (of rb keys) of block j lies: the slice (page * Hkv + head)
   // and *r, the row in it. A bad page (reported where `used`) lies past the last
@@ -334,7 +363,7 @@ struct RunWalker {
 // stored parts is one byte in the workspace header, put back to zero by the last.
 __device__ __forceinline__ bool last_part(uint64_t* stored, uint64_t* counted, int* last_flag, const Segment& seg,
                                           int* ws, int warp, int lane, uint32_t ph, volatile int* abort_flag, int site) {
-  __threadfence();
+  // (The stores are ordered before the fence of warp 0's lane 0 by the barrier.)
   __syncwarp();
   if (lane == 0) mbar_arrive(stored);
   if (warp == 0) {
