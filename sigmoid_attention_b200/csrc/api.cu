@@ -40,9 +40,9 @@ cudaError_t launch_paged_reserve(const PagedReserve& a, int num_sms, cudaStream_
 cudaError_t launch_paged_release(const PagedRelease& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_paged_write(PagedWrite a, int num_sms, cudaStream_t stream);
 cudaError_t launch_paged_many(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttend& a,
-                              int grid, cudaStream_t stream);
+                              bool wide, int grid, cudaStream_t stream);
 cudaError_t launch_paged_few(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttend& a,
-                             int grid, cudaStream_t stream);
+                             bool wide, int grid, cudaStream_t stream);
 void set_last_error(const char* msg);
 }  // namespace sigattn
 
@@ -698,20 +698,25 @@ int sigattn_fwd_paged(const void* q, long long q_stride, const void* k_cache, co
   if (st != SIGATTN_OK || total == 0) return st;
   using bf16 = __nv_bfloat16;
   const int G = Hq / Hkv;
+  const bool few = paged_is_few(Hq, Hkv, max_seqlen_q);
+  // A bound on the call's units of work (paged_run.cuh).
+  const int item = 2 * (128 / G);
+  const double units = static_cast<double>(Hkv) * (max_pages * page_size / 128 + 1) * (few ? B : 2.0 * (total / item + B));
+  const bool wide = units >= 2147483648.0;
   const PagedAttend a{static_cast<const bf16*>(q), static_cast<const bf16*>(k_cache), static_cast<const bf16*>(v_cache),
                       static_cast<bf16*>(o), q_stride, cu_seqlens, kv_lens, block_table, B, Hq, Hkv, max_seqlen_q, total,
-                      max_pages, shift, num_pages, d, causal != 0, paged_is_few(Hq, Hkv, max_seqlen_q) ? 1 : 2,
+                      max_pages, shift, num_pages, d, causal != 0, few ? 1 : 2,
                       reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes),
                       static_cast<int*>(workspace)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool few = paged_is_few(Hq, Hkv, max_seqlen_q);
   CUtensorMap tq, tk, tv;
   if (!make_map_rows(&tq, q, total, Hq, q_stride, d, G, few ? max_seqlen_q : 128 / G) ||
       !make_map(&tk, k_cache, num_pages * Hkv, page_size, d, std::min(page_size, 128)) ||
       !make_map(&tv, v_cache, num_pages * Hkv, page_size, d, std::min(page_size, 128)))
     return map_failure();
   const int grid = std::min(info.num_sms, kMaxPagedCtas);
-  return cuda_status(few ? launch_paged_few(tq, tk, tv, a, grid, s) : launch_paged_many(tq, tk, tv, a, grid, s));
+  return cuda_status(few ? launch_paged_few(tq, tk, tv, a, wide, grid, s)
+                         : launch_paged_many(tq, tk, tv, a, wide, grid, s));
 }
 
 int sigattn_plan(const int32_t* lengths, int B, int H, int Lmax, int d, int kind, void* workspace,

@@ -49,7 +49,7 @@ struct PagedAttend {
   long long q_stride;
   const int *cu, *kv, *table;
   int B, Hq, Hkv, max_q, total, max_pages, page_shift, num_pages, d, causal;
-  int least;     // fewest units of work in a CTA's run
+  int least;     // fewest units of work in a CTA's run (paged_run.cuh)
   float* parts;  // partial sums of tiles cut over CTAs, two places per CTA
   int* ws;
 };

@@ -34,9 +34,9 @@
 //    warps, so the next segment's weights do not wait for it: short texts
 //    took 4200 cycles per segment before, most of them this chain.
 //
-// Roles (16 warps): 0-7 weights, four per group (thread = key), 8-11 output
-// (thread = column of O), 12 the producer (page tables, TMA), 13 the issuer of
-// S^T, 14 and 15 the groups' issuers of O^T.
+// Roles (17 warps): 0-7 weights, four per group (thread = key), 8-11 output
+// (thread = column of O), 12 and 13 the producers of K (and Q) and of V, 14 the
+// issuer of S^T, 15 and 16 the groups' issuers of O^T.
 #include "paged_run.cuh"
 
 namespace sigattn {
@@ -71,7 +71,7 @@ struct FewCfg {
   static constexpr int TM_O = 2 * NR;
   static constexpr int TMEM_COLS = NR == 16 ? 128 : NR == 32 ? 256 : 512;  // >= 6 NR
   static constexpr int EPI_WARPS = 8;
-  static constexpr int kProducer = EPI_WARPS + OUT_WARPS, kIssueS = kProducer + 1, kIssueO = kProducer + 2;
+  static constexpr int kLoadK = EPI_WARPS + OUT_WARPS, kLoadV = kLoadK + 1, kIssueS = kLoadK + 2, kIssueO = kLoadK + 3;
   static constexpr int THREADS = (kIssueO + 2) * 32;
 };
 
@@ -79,13 +79,14 @@ struct FewCfg {
 struct OneTile {
   __device__ __forceinline__ int items(const SeqInfo&) const { return 1; }
   __device__ __forceinline__ int blocks(const SeqInfo& s, int) const { return seq_blocks(s.n); }
-  __device__ __forceinline__ int weight(const SeqInfo&, int) const { return 1; }
-  __device__ __forceinline__ long long before(const SeqInfo& s, int k) const {
-    return static_cast<long long>(k) * seq_blocks(s.n);
+  __device__ __forceinline__ int shift(const SeqInfo&, int) const { return 0; }
+  template <typename U>
+  __device__ __forceinline__ U before(const SeqInfo& s, int k) const {
+    return static_cast<U>(k) * seq_blocks(s.n);
   }
 };
 
-template <int STAGES>
+template <int STAGES, typename U>
 struct FewBarriers {
   uint64_t full[STAGES], empty[STAGES];  // K slots first, then V slots
   uint64_t q_full[2], q_empty[2];
@@ -94,20 +95,21 @@ struct FewBarriers {
   uint64_t o_full[2], o_empty[2];
   uint64_t stored, counted, joined, drain[3];
   SegRing ring;
-  PlanRun run;
+  PlanRun<U> run;
   uint32_t tmem_base;
   int abort, last;
 };
 
 }  // namespace
 
-template <int D, int NR>
+// U: an unsigned type that holds the call's units of work.
+template <int D, int NR, typename U>
 __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     paged_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const PagedAttend a) {
   using C = FewCfg<D, NR>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ FewBarriers<C::STAGES> bar;
+  __shared__ FewBarriers<C::STAGES, U> bar;
   __shared__ float s_log2n[C::EPI_WARPS][NR];  // each epilogue warp's log2 N and N of the segment's rows
   __shared__ int s_seen[C::EPI_WARPS][NR];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -116,14 +118,17 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &bar.abort;
   int* ws = a.ws;
-  constexpr int kProducer = C::kProducer, kIssueS = C::kIssueS, kIssueO = C::kIssueO;
+  constexpr int kLoadK = C::kLoadK, kLoadV = C::kLoadV, kIssueS = C::kIssueS, kIssueO = C::kIssueO;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&bar.full[s], 1);
-      mbar_init(&bar.empty[s], s < C::KST ? 1 : 2);
-    }
-    for (int s = 0; s < 2; ++s) {
+  // The barriers, a few per warp: one thread would take 500 cycles over them.
+  if (lane == 0 && warp < 5) {
+    if (warp == 0) {
+      for (int s = 0; s < C::STAGES; ++s) mbar_init(&bar.full[s], 1);
+      bar.abort = 0;
+    } else if (warp == 1) {
+      for (int s = 0; s < C::STAGES; ++s) mbar_init(&bar.empty[s], s < C::KST ? 1 : 2);
+    } else if (warp < 4) {
+      const int s = warp - 2;
       mbar_init(&bar.q_full[s], 1);
       mbar_init(&bar.q_empty[s], 1);
       mbar_init(&bar.s_full[s], 1);
@@ -132,91 +137,72 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
       mbar_init(&bar.p_empty[s], 1);
       mbar_init(&bar.o_full[s], 2);
       mbar_init(&bar.o_empty[s], C::OUT_WARPS);
+    } else {
+      for (int s = 0; s < 3; ++s) mbar_init(&bar.drain[s], 1);
+      mbar_init(&bar.stored, C::OUT_WARPS);
+      mbar_init(&bar.counted, 1);
+      mbar_init(&bar.joined, C::OUT_WARPS);
+      seg_ring_init(bar.ring, C::EPI_WARPS + C::OUT_WARPS + 3);
     }
-    for (int s = 0; s < 3; ++s) mbar_init(&bar.drain[s], 1);
-    mbar_init(&bar.stored, C::OUT_WARPS);
-    mbar_init(&bar.counted, 1);
-    mbar_init(&bar.joined, C::OUT_WARPS);
-    seg_ring_init(bar.ring, C::EPI_WARPS + C::OUT_WARPS + 3);
-    bar.abort = 0;
     fence_mbar_init();
   }
   if (warp == kIssueO) {
     tmem_alloc(&bar.tmem_base, C::TMEM_COLS);
     tmem_relinquish();
   }
+  if (lane == 0 && warp == kLoadK) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+  }
+  if (lane == 0 && warp == kLoadV) tma_prefetch_desc(&tm_v);
   // Query rows that no load covers stay zero.
   for (int i = threadIdx.x; i < 2 * C::Q_BYTES / 16; i += C::THREADS)
     reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   grid_dep_launch();
   grid_dep_wait();
-  plan_run<C::THREADS>(a, &bar.run, [](const SeqInfo& s) { return seq_blocks(s.n); });
+  plan_run<C::THREADS>(a, &bar.run, [](const SeqInfo& s) -> U { return seq_blocks(s.n); });
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem_base;
   const int G = a.Hq / a.Hkv;
 
-  if (warp == kProducer) {
-    // ------------------------------------------------------------- producer
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-    }
-    const int rb = min(1 << a.page_shift, kKeyBlock);  // keys per box
-    const int q_bytes = min(a.max_q * G, NR) * 128 * C::CH;
-    uint32_t qb = 0, qph = 0, rst = 0, rph = 0;
-    uint32_t loads[2] = {0, 0}, q_used = 0;  // K, V and Q tiles loaded, for an aborting producer
-    uint32_t st[2] = {0, 0}, ph[2] = {0, 0};
-    bool ok = true;
+  if (warp == kLoadK || warp == kLoadV) {
+    // ------------------------------------- producers: segments, Q and K; V
+    // Both walk the run; the K warp hands its segments to the other roles.
+    const bool is_k = warp == kLoadK;
     const OneTile tiles{};
-    RunWalker<OneTile> walk(a, tiles, bar.run, lane);
+    RunWalker<U, OneTile> walk(a, tiles, bar.run, lane);
     const Segment& seg = walk.seg;
-    for (; ok && walk.alive; walk.next()) {
-      if (!(ok = seg_publish(bar.ring, rst, rph, seg, lane, abort_flag, ws, 300))) break;
-      if (!(ok = warp_wait(&bar.q_empty[qb], qph ^ 1, abort_flag, ws, 301))) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bar.q_full[qb], q_bytes);
-        for (int c = 0; c < C::CH; ++c)
-          tma_load_3d(sQ + qb * C::Q_BYTES + c * C::Q_CHUNK, &tm_q, &bar.q_full[qb], c * 64, seg.head * G, seg.start);
-      }
-      ++q_used;
-      if ((qb ^= 1) == 0) qph ^= 1;
-      for (int j = seg.j0; ok && j < seg.j1; ++j) {
-        const int keys = min(kKeyBlock, seg.n - j * kKeyBlock);
-        const int boxes = (keys + rb - 1) / rb;  // 0 for a sequence without keys
-        int row;
-        const int z = walk.locate(j, lane / C::CH, rb, lane / C::CH < boxes, &row);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t slot = (kv ? C::KST : 0) + st[kv];
-          if (!(ok = warp_wait(&bar.empty[slot], ph[kv] ^ 1, abort_flag, ws, 302))) break;
-          if (lane == 0) mbar_arrive_expect_tx(&bar.full[slot], boxes * rb * 128 * C::CH);
-          __syncwarp();
-          if (lane < boxes * C::CH)
-            tma_load_3d(smem + slot * C::TILE_BYTES + (lane % C::CH) * C::BOX_BYTES + (lane / C::CH) * rb * 128,
-                        kv ? &tm_v : &tm_k, &bar.full[slot], (lane % C::CH) * 64, row, z);
-          __syncwarp();
-          ++loads[kv];
-          if (++st[kv] == (kv ? C::VST : C::KST)) { st[kv] = 0; ph[kv] ^= 1; }
+    TileRing<D> ring{is_k ? &tm_k : &tm_v, smem + (is_k ? 0 : C::KST * C::TILE_BYTES), bar.full + (is_k ? 0 : C::KST),
+                     bar.empty + (is_k ? 0 : C::KST), is_k ? C::KST : C::VST, 1 << walk.box_shift(), 0, 0, 0};
+    const int q_bytes = min(a.max_q * G, NR) * 128 * C::CH;
+    uint32_t qb = 0, qph = 0, rst = 0, rph = 0, q_used = 0;
+    bool ok = true;
+    while (ok && walk.advance()) {
+      if (is_k) {
+        if (!(ok = seg_publish(bar.ring, rst, rph, seg, lane, abort_flag, ws, 300))) break;
+        if (!(ok = warp_wait(&bar.q_empty[qb], qph ^ 1, abort_flag, ws, 301))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bar.q_full[qb], q_bytes);
+          for (int c = 0; c < C::CH; ++c)
+            tma_load_3d(sQ + qb * C::Q_BYTES + c * C::Q_CHUNK, &tm_q, &bar.q_full[qb], c * 64, seg.head * G, seg.start);
         }
+        ++q_used;
+        if ((qb ^= 1) == 0) qph ^= 1;
+      }
+      for (int j = seg.j0; ok && j < seg.j1; ++j) {
+        ok = ring.load(walk, j, lane, abort_flag, ws, is_k ? 302 : 304);
+        if (j == seg.j0) walk.prefetch();
       }
     }
-    if (ok) ok = seg_publish(bar.ring, rst, rph, end_segment(), lane, abort_flag, ws, 303);
-    if (!ok) {  // aborting: let the copies in flight land before the CTA exits
+    if (ok && is_k) ok = seg_publish(bar.ring, rst, rph, end_segment(), lane, abort_flag, ws, 303);
+    if (!ok) {
+      ring.settle();
       int never = 0;
-      volatile int* no_abort = &never;
-      for (int kv = 0; kv < 2; ++kv) {
-        const uint32_t slots = kv ? C::VST : C::KST;
-        for (uint32_t s = 0; s < slots && s < loads[kv]; ++s) {
-          const uint32_t idx = loads[kv] - 1 - s;
-          mbar_wait(&bar.full[(kv ? C::KST : 0) + idx % slots], (idx / slots) & 1, no_abort, nullptr, 0);
-        }
-      }
       for (uint32_t s = 0; s < 2 && s < q_used; ++s)
-        mbar_wait(&bar.q_full[(q_used - 1 - s) & 1], ((q_used - 1 - s) >> 1) & 1, no_abort, nullptr, 0);
+        mbar_wait(&bar.q_full[(q_used - 1 - s) & 1], ((q_used - 1 - s) >> 1) & 1, &never, nullptr, 0);
     }
   } else if (warp == kIssueS) {
     // ------------------------------------------------- S^T = K Q^T (128 x NR)
@@ -355,41 +341,44 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
         if ((t & 1) != static_cast<uint32_t>(g)) continue;
         if (!(ok = warp_wait(&bar.s_full[g], sph, abort_flag, ws, 331))) break;
         tc_fence_after();
-        uint32_t s[NR];
-        if constexpr (NR == 16) {
-          tmem_ld16(tmem + lane_off + C::TM_S + g * NR, s);
-        } else {
+        const bool cut = (j + 1) * kKeyBlock > least;
+        const int at = j * kKeyBlock + key;
+        // 32 columns at a time at most
+        constexpr int W = NR < 32 ? NR : 32;
 #pragma unroll
-          for (int c = 0; c < NR / 32; ++c)
-            tmem_ld32(tmem + lane_off + C::TM_S + g * NR + 32 * c, reinterpret_cast<uint32_t(&)[32]>(s[32 * c]));
+        for (int c0 = 0; c0 < NR; c0 += W) {
+          uint32_t s[W];
+          tmem_ld_cols(tmem + lane_off + C::TM_S + g * NR + c0, s);
+          if (c0 + W == NR) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.s_empty[g]);
+          }
+          if (cut) {
+#pragma unroll
+            for (int n = 0; n < W; ++n)
+              if (at >= my_seen[c0 + n]) s[n] = 0xff800000u;  // -inf: weight 0
+          }
+          // sigma(x) = 1 / (1 + 2^(log2 N - s scale log2 e)). Two MUFU operations
+          // per weight, which this kernel's few weights allow: both are exact to
+          // about 1e-7, where the polynomial of the whole-sequence kernels
+          // (sigmoid_n) spends 9e-4.
+#pragma unroll
+          for (int n = 0; n < W; ++n)
+            s[n] = __float_as_uint(rcp_approx(
+                1.0f + ex2_approx(fmaf(__uint_as_float(s[n]), -scale_l2e, my_log2n[c0 + n]))));
+          if (c0 == 0 && !(ok = warp_wait(&bar.p_empty[g], pph ^ 1, abort_flag, ws, 332))) break;
+#pragma unroll
+          for (int c = 0; c < W / 8; ++c) {
+            const uint32_t* w = s + 8 * c;
+            *reinterpret_cast<uint4*>(prow + (((c0 / 8 + c) ^ (key & 7)) << 4)) =
+                make_uint4(pack_bf16x2(__uint_as_float(w[0]), __uint_as_float(w[1])),
+                           pack_bf16x2(__uint_as_float(w[2]), __uint_as_float(w[3])),
+                           pack_bf16x2(__uint_as_float(w[4]), __uint_as_float(w[5])),
+                           pack_bf16x2(__uint_as_float(w[6]), __uint_as_float(w[7])));
+          }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.s_empty[g]);
-        if ((j + 1) * kKeyBlock > least) {
-          const int at = j * kKeyBlock + key;
-#pragma unroll
-          for (int n = 0; n < NR; ++n)
-            if (at >= my_seen[n]) s[n] = 0xff800000u;  // -inf: weight 0
-        }
-        // sigma(x) = 1 / (1 + 2^(log2 N - s scale log2 e)). Two MUFU operations
-        // per weight, which this kernel's few weights allow: both are exact to
-        // about 1e-7, where the polynomial of the whole-sequence kernels
-        // (sigmoid_n) spends 9e-4.
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-          s[n] = __float_as_uint(rcp_approx(
-              1.0f + ex2_approx(fmaf(__uint_as_float(s[n]), -scale_l2e, my_log2n[n]))));
-        if (!(ok = warp_wait(&bar.p_empty[g], pph ^ 1, abort_flag, ws, 332))) break;
-#pragma unroll
-        for (int c = 0; c < NR / 8; ++c) {
-          const uint32_t* w = s + 8 * c;
-          *reinterpret_cast<uint4*>(prow + ((c ^ (key & 7)) << 4)) =
-              make_uint4(pack_bf16x2(__uint_as_float(w[0]), __uint_as_float(w[1])),
-                         pack_bf16x2(__uint_as_float(w[2]), __uint_as_float(w[3])),
-                         pack_bf16x2(__uint_as_float(w[4]), __uint_as_float(w[5])),
-                         pack_bf16x2(__uint_as_float(w[6]), __uint_as_float(w[7])));
-        }
+        if (!ok) break;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[g]);
@@ -416,7 +405,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     // time. Lanes take four columns each, so a warp reads SUB rows of a part at
     // once; part p belongs to slice p % SLICES, the slices are added in order.
     auto join = [&](const Segment& seg, int rows) -> bool {
-      constexpr int LPR = C::LPR, SLICES = C::SLICES, RC = C::RC, UNROLL = 4;
+      constexpr int LPR = C::LPR, SLICES = C::SLICES, RC = C::RC, UNROLL = 3;
       const int np = seg.last_cta - seg.first_cta + 1;
       const int slice = ow * C::SUB + lane / LPR, l4 = lane % LPR;
       float4* red = reinterpret_cast<float4*>(smem + C::OFF_RED);
@@ -533,31 +522,38 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
 
 namespace {
 
-template <int D, int NR>
+template <int D, int NR, typename U>
 cudaError_t launch_few_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttend& a,
                             int grid, cudaStream_t stream) {
   using C = FewCfg<D, NR>;
   static PerDeviceOnce attr;
   const cudaError_t e = attr.run([] {
-    return cudaFuncSetAttribute(paged_few_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
+    return cudaFuncSetAttribute(paged_few_kernel<D, NR, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
   });
   if (e != cudaSuccess) return e;
-  return launch_programmatic(paged_few_kernel<D, NR>, dim3(grid), dim3(C::THREADS), C::SMEM_ALLOC, stream, tq, tk, tv, a);
+  return launch_programmatic(paged_few_kernel<D, NR, U>, dim3(grid), dim3(C::THREADS), C::SMEM_ALLOC, stream, tq, tk, tv,
+                             a);
+}
+
+template <typename U, typename... Args>
+cudaError_t launch_few(int d, int rows, Args&&... args) {
+  if (d == 64) {
+    if (rows <= 16) return launch_few_impl<64, 16, U>(args...);
+    if (rows <= 32) return launch_few_impl<64, 32, U>(args...);
+    return launch_few_impl<64, 64, U>(args...);
+  }
+  if (rows <= 16) return launch_few_impl<128, 16, U>(args...);
+  if (rows <= 32) return launch_few_impl<128, 32, U>(args...);
+  return launch_few_impl<128, 64, U>(args...);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_few(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttend& a,
-                             int grid, cudaStream_t stream) {
+                             bool wide, int grid, cudaStream_t stream) {
   const int rows = a.max_q * (a.Hq / a.Hkv);
-  if (a.d == 64) {
-    if (rows <= 16) return launch_few_impl<64, 16>(tq, tk, tv, a, grid, stream);
-    if (rows <= 32) return launch_few_impl<64, 32>(tq, tk, tv, a, grid, stream);
-    return launch_few_impl<64, 64>(tq, tk, tv, a, grid, stream);
-  }
-  if (rows <= 16) return launch_few_impl<128, 16>(tq, tk, tv, a, grid, stream);
-  if (rows <= 32) return launch_few_impl<128, 32>(tq, tk, tv, a, grid, stream);
-  return launch_few_impl<128, 64>(tq, tk, tv, a, grid, stream);
+  return wide ? launch_few<unsigned long long>(a.d, rows, tq, tk, tv, a, grid, stream)
+              : launch_few<uint32_t>(a.d, rows, tq, tk, tv, a, grid, stream);
 }
 
 }  // namespace sigattn

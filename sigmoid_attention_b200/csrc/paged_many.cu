@@ -25,9 +25,9 @@
 //    chain S, weights, PV on every block. Issuer 0 then issues all products, so
 //    that all of them add to one O in order.
 //
-// Roles (19 warps): 0-15 epilogue (warps 0-7 tile 0, 8-15 tile 1; per tile, four
-// warps for each half of a block's keys), 16 the producer, 17 and 18 the
-// issuers of tiles 0 and 1.
+// Roles (20 warps): 0-15 epilogue (warps 0-7 tile 0, 8-15 tile 1; per tile, four
+// warps for each half of a block's keys), 16 and 17 the producers of K (and Q) and
+// of V, 18 and 19 the issuers of tiles 0 and 1.
 // TMEM: S of tile t at columns [128t, 128t + 128), O at 256 + t D; P over S
 // (d = 128) or in a region of its own after O (d = 64).
 #include "paged_run.cuh"
@@ -51,10 +51,10 @@ struct ManyCfg {
   static constexpr int TM_S = 0, TM_O = 256, TM_P = TM_O + 2 * D;
   static constexpr int TMEM_COLS = 512;
   static constexpr int EPI_WARPS = 16;
-  static constexpr int THREADS = (EPI_WARPS + 3) * 32;
+  static constexpr int THREADS = (EPI_WARPS + 4) * 32;
 };
 
-template <int QST, int KST, int VST>
+template <int QST, int KST, int VST, typename U>
 struct ManyBarriers {
   uint64_t q_full[QST], q_empty[QST];
   uint64_t k_full[KST], k_empty[KST];
@@ -66,26 +66,40 @@ struct ManyBarriers {
   uint64_t fin[2][4];    // issuer t's products of a segment completed (by segment, modulo 4)
   uint64_t stored, counted, drain[2];
   SegRing ring;
-  PlanRun run;
+  PlanRun<U> run;
   uint32_t tmem_base;
   int abort, last;
 };
 
-// sum_{k < n} floor((x k + y) / 128): after taking out whole parts, the lattice
-// points under the line are counted along the other axis. x n and y are at most
-// twice the longest sequence, so only the sum needs 64 bits.
-__device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t x, uint32_t y) {
+// sum_{k < n} floor((x k + y) / 128), x n and y less than 2^25. Where x is a power
+// of two (G is one) the sum has a closed form; otherwise, after taking out whole
+// parts, the lattice points under the line are counted along the other axis.
+template <typename U>
+__device__ __forceinline__ U floor_sum(uint32_t n, uint32_t x, uint32_t y) {
+  // Half of an even product (halved first: U may hold the sum but not its terms,
+  // which is harmless where each step is exact modulo its size).
+  auto half = [](uint32_t v, uint32_t w) { return (v & 1) ? static_cast<U>(v) * (w >> 1) : static_cast<U>(v >> 1) * w; };
+  if ((x & (x - 1)) == 0) {
+    const int e = 31 - __clz(x);
+    if (e >= 7) return (half(n, n - 1) << (e - 7)) + static_cast<U>(n) * (y >> 7);
+    const int f = 7 - e;  // floor((x k + y) / 128) = floor((k + (y >> e)) / 2^f)
+    auto upto = [&](uint32_t k) {
+      const uint32_t t = k >> f;
+      return (half(t, t - 1) << f) + static_cast<U>(t) * (k & ((1u << f) - 1));
+    };
+    return upto((y >> e) + n) - upto(y >> e);
+  }
   uint32_t m = kKeyBlock;
-  long long sum = 0;
+  U sum = 0;
   while (n > 0) {
     if (x >= m) {
       const uint32_t q = x / m;
-      sum += static_cast<long long>(n) * (n - 1) / 2 * q;
+      sum += half(n, n - 1) * q;
       x -= q * m;
     }
     if (y >= m) {
       const uint32_t q = y / m;
-      sum += static_cast<long long>(n) * q;
+      sum += static_cast<U>(n) * q;
       y -= q * m;
     }
     const uint32_t top = x * n + y;
@@ -100,14 +114,15 @@ __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t x, uint32_t 
 }
 
 // A sequence's tiles: an item is two query tiles, 2 T tokens (the last may be
-// one). A block of an item weighs as many units as it has tiles: two tiles'
-// products bound a block, one tile's are about as fast as its keys arrive, in
-// half the time.
+// one). A block of an item is as many units as it has tiles: two tiles' products
+// bound a block, one tile's are about as fast as its keys arrive, in half the
+// time.
 struct TileMath {
   int T;
   int causal;
   __device__ __forceinline__ int items(const SeqInfo& s) const { return (s.m + 2 * T - 1) / (2 * T); }
-  __device__ __forceinline__ int weight(const SeqInfo& s, int k) const { return k * 2 * T + T < s.m ? 2 : 1; }
+  __device__ __forceinline__ bool two(const SeqInfo& s, int k) const { return k * 2 * T + T < s.m; }
+  __device__ __forceinline__ int shift(const SeqInfo& s, int k) const { return two(s, k) ? 1 : 0; }
   // Keys that token i sees.
   __device__ __forceinline__ int seen(int m, int n, int i) const {
     return causal ? max(0, min(n, n - m + i + 1)) : n;
@@ -118,18 +133,19 @@ struct TileMath {
     return blocks(s.m, s.n, min((k + 1) * 2 * T, s.m) - 1);
   }
   // Units of items 0 .. k - 1 (k <= items).
-  __device__ __forceinline__ long long before(const SeqInfo& s, int k) const {
-    long long sum = 0;
+  template <typename U>
+  __device__ __forceinline__ U before(const SeqInfo& s, int k) const {
+    U sum = 0;
     if (k > 0 && k == items(s)) {  // the last item may hold fewer tokens
       --k;
-      sum = static_cast<long long>(seq_blocks(s.n)) * weight(s, k);
+      sum = static_cast<U>(seq_blocks(s.n)) << shift(s, k);
     }
-    if (!causal) return sum + 2ll * k * seq_blocks(s.n);
-    // Item i's last token sees x(i) = n - m + (i + 1) 2 T keys; where x <= 0 it
-    // walks the one block that writes its zeros.
+    if (!causal) return sum + 2 * static_cast<U>(k) * seq_blocks(s.n);
+    // Item i's last token sees n - m + (i + 1) 2 T keys, or (more rows than
+    // tokens) none: then it still walks the block that writes its zeros.
     const int item = 2 * T, c = s.n - s.m;
     const int none = c < 0 ? min(k, -c / item) : 0;
-    return sum + 2ll * none + 2 * floor_sum(k - none, item, c + (none + 1) * item + kKeyBlock - 1);
+    return sum + 2 * (static_cast<U>(none) + floor_sum<U>(k - none, item, c + (none + 1) * item + kKeyBlock - 1));
   }
 };
 
@@ -142,13 +158,14 @@ struct Shape {
 
 }  // namespace
 
-template <int D>
+// U: an unsigned type that holds the call's units of work.
+template <int D, typename U>
 __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
     paged_many_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const PagedAttend a) {
   using C = ManyCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ ManyBarriers<C::QST, C::KST, C::VST> bar;
+  __shared__ ManyBarriers<C::QST, C::KST, C::VST, U> bar;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sK = smem + C::OFF_K;
@@ -156,13 +173,19 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &bar.abort;
   int* ws = a.ws;
-  constexpr int kProducer = C::EPI_WARPS, kIssuer = C::EPI_WARPS + 1;
+  constexpr int kLoadK = C::EPI_WARPS, kLoadV = kLoadK + 1, kIssuer = kLoadK + 2;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::QST; ++s) { mbar_init(&bar.q_full[s], 1); mbar_init(&bar.q_empty[s], 2); }
-    for (int s = 0; s < C::KST; ++s) { mbar_init(&bar.k_full[s], 1); mbar_init(&bar.k_empty[s], 2); }
-    for (int s = 0; s < C::VST; ++s) { mbar_init(&bar.v_full[s], 1); mbar_init(&bar.v_empty[s], 2); }
-    for (int t = 0; t < 2; ++t) {
+  // The barriers, a few per warp: one thread would take 600 cycles over them.
+  if (lane == 0 && warp < 7) {
+    if (warp == 0) {
+      for (int s = 0; s < C::QST; ++s) { mbar_init(&bar.q_full[s], 1); mbar_init(&bar.q_empty[s], 2); }
+      bar.abort = 0;
+    } else if (warp == 1) {
+      for (int s = 0; s < C::KST; ++s) { mbar_init(&bar.k_full[s], 1); mbar_init(&bar.k_empty[s], 2); }
+    } else if (warp == 2) {
+      for (int s = 0; s < C::VST; ++s) { mbar_init(&bar.v_full[s], 1); mbar_init(&bar.v_empty[s], 2); }
+    } else if (warp < 5) {
+      const int t = warp - 3;
       mbar_init(&bar.s_full[t], 1);
       mbar_init(&bar.p_full[2 * t], 4);
       mbar_init(&bar.p_full[2 * t + 1], 4);
@@ -172,24 +195,30 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
       mbar_init(&bar.s_read[t], 8);
       mbar_init(&bar.pv_done[t], 1);
       mbar_init(&bar.drain[t], 1);
-      for (int s = 0; s < 4; ++s) mbar_init(&bar.fin[t][s], 1);
+    } else if (warp == 5) {
+      for (int s = 0; s < 4; ++s) { mbar_init(&bar.fin[0][s], 1); mbar_init(&bar.fin[1][s], 1); }
+    } else {
+      mbar_init(&bar.stored, C::EPI_WARPS);
+      mbar_init(&bar.counted, 1);
+      seg_ring_init(bar.ring, C::EPI_WARPS + 2);
     }
-    mbar_init(&bar.stored, C::EPI_WARPS);
-    mbar_init(&bar.counted, 1);
-    seg_ring_init(bar.ring, C::EPI_WARPS + 2);
-    bar.abort = 0;
     fence_mbar_init();
   }
   if (warp == kIssuer) {
     tmem_alloc(&bar.tmem_base, C::TMEM_COLS);
     tmem_relinquish();
   }
+  if (lane == 0 && warp == kLoadK) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+  }
+  if (lane == 0 && warp == kLoadV) tma_prefetch_desc(&tm_v);
   const int G = a.Hq / a.Hkv;
   const int T = 128 / G;  // tokens per tile
   const TileMath math{T, a.causal};
   grid_dep_launch();
   grid_dep_wait();
-  plan_run<C::THREADS>(a, &bar.run, [&](const SeqInfo& s) { return math.before(s, math.items(s)); });
+  plan_run<C::THREADS>(a, &bar.run, [&](const SeqInfo& s) { return math.before<U>(s, math.items(s)); });
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -207,69 +236,45 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
     return max(seg.j0, min(seg.j1, math.blocks(seg.m, seg.n, min(i0 + T, seg.m) - 1)));
   };
 
-  if (warp == kProducer) {
-    // ------------------------------------------------------------- producer
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-    }
-    const int rb = min(1 << a.page_shift, kKeyBlock);  // keys per box
-    uint32_t rst = 0, rph = 0, qst = 0, qph = 0, q_loads = 0;
-    uint32_t st[2] = {0, 0}, ph[2] = {0, 0}, loads[2] = {0, 0};
-    bool ok = true;
-    RunWalker<TileMath> walk(a, math, bar.run, lane);
+  if (warp == kLoadK || warp == kLoadV) {
+    // ------------------------------------- producers: segments, Q and K; V
+    // Both walk the run; the K warp hands its segments to the other roles.
+    const bool is_k = warp == kLoadK;
+    RunWalker<U, TileMath> walk(a, math, bar.run, lane);
     const Segment& seg = walk.seg;
-    for (; ok && walk.alive; walk.next()) {
-      if (!(ok = seg_publish(bar.ring, rst, rph, seg, lane, abort_flag, ws, 400))) break;
-      const int i0 = seg.tile * 2 * T, ntiles = i0 + T < seg.m ? 2 : 1;
-      for (int t = 0; ok && t < ntiles; ++t) {
-        if (!(ok = warp_wait(&bar.q_empty[qst], qph ^ 1, abort_flag, ws, 401))) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bar.q_full[qst], T * G * 128 * C::CH);
-          for (int c = 0; c < C::CH; ++c)
-            tma_load_3d(sQ + qst * C::TILE_BYTES + c * C::BOX_BYTES, &tm_q, &bar.q_full[qst], c * 64, seg.head * G,
-                        seg.start + i0 + t * T);
+    TileRing<D> ring{is_k ? &tm_k : &tm_v, is_k ? sK : sV, is_k ? bar.k_full : bar.v_full, is_k ? bar.k_empty : bar.v_empty,
+                     is_k ? C::KST : C::VST, 1 << walk.box_shift(), 0, 0, 0};
+    uint32_t rst = 0, rph = 0, qst = 0, qph = 0, q_loads = 0;
+    bool ok = true;
+    while (ok && walk.advance()) {
+      if (is_k) {
+        if (!(ok = seg_publish(bar.ring, rst, rph, seg, lane, abort_flag, ws, 400))) break;
+        const int i0 = seg.tile * 2 * T, ntiles = i0 + T < seg.m ? 2 : 1;
+        for (int t = 0; ok && t < ntiles; ++t) {
+          if (!(ok = warp_wait(&bar.q_empty[qst], qph ^ 1, abort_flag, ws, 401))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bar.q_full[qst], T * G * 128 * C::CH);
+            for (int c = 0; c < C::CH; ++c)
+              tma_load_3d(sQ + qst * C::TILE_BYTES + c * C::BOX_BYTES, &tm_q, &bar.q_full[qst], c * 64, seg.head * G,
+                          seg.start + i0 + t * T);
+          }
+          __syncwarp();
+          ++q_loads;
+          if (++qst == C::QST) { qst = 0; qph ^= 1; }
         }
-        __syncwarp();
-        ++q_loads;
-        if (++qst == C::QST) { qst = 0; qph ^= 1; }
       }
       for (int j = seg.j0; ok && j < seg.j1; ++j) {
-        const int keys = min(kKeyBlock, seg.n - j * kKeyBlock);
-        const int boxes = (keys + rb - 1) / rb;  // 0 for a sequence without keys
-        int row;
-        const int z = walk.locate(j, lane / C::CH, rb, lane / C::CH < boxes, &row);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          uint64_t* full = kv ? &bar.v_full[st[1]] : &bar.k_full[st[0]];
-          if (!(ok = warp_wait(kv ? &bar.v_empty[st[1]] : &bar.k_empty[st[0]], ph[kv] ^ 1, abort_flag, ws, 402))) break;
-          if (lane == 0) mbar_arrive_expect_tx(full, boxes * rb * 128 * C::CH);
-          __syncwarp();
-          if (lane < boxes * C::CH)
-            tma_load_3d((kv ? sV : sK) + st[kv] * C::TILE_BYTES + (lane % C::CH) * C::BOX_BYTES +
-                            (lane / C::CH) * rb * 128,
-                        kv ? &tm_v : &tm_k, full, (lane % C::CH) * 64, row, z);
-          __syncwarp();
-          ++loads[kv];
-          if (++st[kv] == (kv ? C::VST : C::KST)) { st[kv] = 0; ph[kv] ^= 1; }
-        }
+        ok = ring.load(walk, j, lane, abort_flag, ws, is_k ? 402 : 404);
+        if (j == seg.j0) walk.prefetch();
       }
     }
-    if (ok) ok = seg_publish(bar.ring, rst, rph, end_segment(), lane, abort_flag, ws, 403);
-    if (!ok) {  // aborting: let the copies in flight land before the CTA exits
+    if (ok && is_k) ok = seg_publish(bar.ring, rst, rph, end_segment(), lane, abort_flag, ws, 403);
+    if (!ok) {
+      ring.settle();
       int never = 0;
-      volatile int* no_abort = &never;
-      for (int kv = 0; kv < 2; ++kv) {
-        const uint32_t slots = kv ? C::VST : C::KST;
-        for (uint32_t x = 0; x < slots && x < loads[kv]; ++x) {
-          const uint32_t idx = loads[kv] - 1 - x;
-          mbar_wait(kv ? &bar.v_full[idx % slots] : &bar.k_full[idx % slots], (idx / slots) & 1, no_abort, nullptr, 0);
-        }
-      }
       for (uint32_t x = 0; x < C::QST && x < q_loads; ++x) {
         const uint32_t idx = q_loads - 1 - x;
-        mbar_wait(&bar.q_full[idx % C::QST], (idx / C::QST) & 1, no_abort, nullptr, 0);
+        mbar_wait(&bar.q_full[idx % C::QST], (idx / C::QST) & 1, &never, nullptr, 0);
       }
     }
   } else if (warp >= kIssuer) {
@@ -566,7 +571,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         // CTA's first. Parts that start past the tile's last block are not there.
         const int all = math.blocks(seg.m, seg.n, min(token - of + T, seg.m) - 1);
         int np = 1;
-        while (np <= seg.last_cta - seg.first_cta && part_begin(seg, np, bar.run.per, out.two ? 2 : 1) < all) ++np;
+        while (np <= seg.last_cta - seg.first_cta && part_begin(seg, np, bar.run.per, out.two ? 1 : 0) < all) ++np;
         const float* from = a.parts + (2 * seg.first_cta + 1) * kPart + mine;
         for (int c = 0; c < D / 32; ++c, from += 4 * 512) {
           float4 sum[4];
@@ -609,24 +614,26 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
 
 namespace {
 
-template <int D>
+template <int D, typename U>
 cudaError_t launch_many_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttend& a,
                              int grid, cudaStream_t stream) {
   using C = ManyCfg<D>;
   static PerDeviceOnce attr;
   const cudaError_t e = attr.run([] {
-    return cudaFuncSetAttribute(paged_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
+    return cudaFuncSetAttribute(paged_many_kernel<D, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
   });
   if (e != cudaSuccess) return e;
-  return launch_programmatic(paged_many_kernel<D>, dim3(grid), dim3(C::THREADS), C::SMEM_ALLOC, stream, tq, tk, tv, a);
+  return launch_programmatic(paged_many_kernel<D, U>, dim3(grid), dim3(C::THREADS), C::SMEM_ALLOC, stream, tq, tk, tv, a);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_many(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttend& a,
-                              int grid, cudaStream_t stream) {
-  return a.d == 64 ? launch_many_impl<64>(tq, tk, tv, a, grid, stream)
-                   : launch_many_impl<128>(tq, tk, tv, a, grid, stream);
+                              bool wide, int grid, cudaStream_t stream) {
+  using W = unsigned long long;
+  if (a.d == 64)
+    return wide ? launch_many_impl<64, W>(tq, tk, tv, a, grid, stream) : launch_many_impl<64, uint32_t>(tq, tk, tv, a, grid, stream);
+  return wide ? launch_many_impl<128, W>(tq, tk, tv, a, grid, stream) : launch_many_impl<128, uint32_t>(tq, tk, tv, a, grid, stream);
 }
 
 }  // namespace sigattn

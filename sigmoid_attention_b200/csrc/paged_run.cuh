@@ -1,15 +1,17 @@
 // paged_run.cuh -- how the paged attention kernels share a call's work out.
 //
-// A call's units of work (blocks of 128 keys of one query tile of one key/value
-// head of one sequence) stand in one line: sequences in batch order, heads,
+// A call's work (the key blocks that the query tiles of each key/value head of
+// each sequence walk) stands in one line: sequences in batch order, heads,
 // tiles, blocks. The line is cut into equal runs, one per CTA. Each CTA finds
 // its run itself (plan_run: a prefix sum over the batch's lengths), its
 // producer walks it and hands every segment (the part of one tile's blocks
 // that lies in the run) to the other roles through a ring in shared memory.
 // A tile whose blocks lie in several CTAs is joined by the CTA that stores
 // its part last (last_part).
-// Blocks may weigh 1 or 2 units (a block for one query tile or for two); a block
-// belongs to the CTA in whose run its first unit lies.
+// Blocks are 1 or 2 units long (a block for one query tile or for two); a block
+// belongs to the CTA in whose run its first unit lies. (Units of keys, so that
+// texts' last blocks count by their keys, were tried: a short block takes as
+// long as a full one, and 432 groups of 35 to 143 keys took 21 instead of 15 us.)
 #pragma once
 
 #include <climits>
@@ -54,72 +56,69 @@ __device__ __forceinline__ bool seq_check(const PagedAttend& a, const SeqWords& 
   return ok;
 }
 
-// x / y of nonnegative numbers: unit counts nearly always fit 32 bits, where a
-// division takes a fraction of the time.
-__device__ __forceinline__ long long fast_div(long long x, long long y) {
-  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-  return x / y;
-}
-
 // A CTA's run: `count` units from unit blockIdx.x * per of the line on, which is
 // unit `rem` of sequence b.
+template <typename U>
 struct PlanRun {
-  long long rem;
+  U rem;
   SeqInfo s;
   int b, count, per;
 };
 
 // units(s): units of one key/value head of a sequence with new tokens. Runs are
-// at least a.least units long (at least a block's weight, so that a tile's CTAs
-// all have a block of it).
+// at least a.least units long (at least a block's, so that a tile's CTAs all
+// have a block of it). U: an unsigned type that holds the call's units; the
+// usual 32 bits make this half as long as 64.
 // Ends before the caller's next barrier; every thread of the CTA takes part.
-template <int THREADS, typename Units>
-__device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun* run, Units units) {
-  static_assert(THREADS % 32 == 0, "whole warps");
-  __shared__ long long sums[THREADS / 32];
+template <int THREADS, typename U, typename Units>
+__device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun<U>* run, Units units) {
+  constexpr int kWarps = THREADS / 32;
+  static_assert(THREADS % 32 == 0 && kWarps <= 32, "whole warps");
+  __shared__ U sums[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int chunk = ceil_div(a.B, THREADS);
   const int b0 = min(a.B, tid * chunk), b1 = min(a.B, b0 + chunk);
   SeqInfo s;  // of the sequence that units_of saw last
-  auto units_of = [&](int b, bool report) -> long long {
+  auto units_of = [&](int b, bool report) -> U {
     if (!seq_check(a, seq_load(a, b), &s)) {
       if (report && blockIdx.x == 0) raise_invalid(a.ws, -(b + 1));
       return 0;
     }
-    return s.m > 0 ? static_cast<long long>(units(s)) * a.Hkv : 0;
+    return s.m > 0 ? units(s) * static_cast<U>(a.Hkv) : 0;
   };
-  long long mine = 0;
+  U mine = 0;
   for (int b = b0; b < b1; ++b) mine += units_of(b, true);
-  long long incl = mine;
+  auto scan = [&](U v) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += u;
-  }
+    for (int o = 1; o < 32; o <<= 1) {
+      const U u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    return v;
+  };
+  const U incl = scan(mine);
   if (lane == 31) sums[warp] = incl;
   __syncthreads();
-  long long base = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w == warp) base = total;
-    total += sums[w];
-  }
-  base += incl - mine;
-  long long per = max(static_cast<long long>(a.least), fast_div(total + gridDim.x - 1, gridDim.x));
+  const U upto = scan(lane < kWarps ? sums[lane] : 0);
+  const U total = __shfl_sync(0xffffffffu, upto, kWarps - 1);
+  const U before = __shfl_sync(0xffffffffu, upto, warp > 0 ? warp - 1 : 0);
+  const U base = (warp > 0 ? before : 0) + incl - mine;
+  U per = max(static_cast<U>(a.least), (total + gridDim.x - 1) / gridDim.x);
+  U left = total;
   if (per > INT_MAX) {  // beyond any call that could end
     if (blockIdx.x == 0 && tid == 0) raise_invalid(a.ws, 206);
-    per = total = 0;
+    per = left = 0;
   }
-  const long long first = min(total, per * blockIdx.x);
+  const U first = min(left, per * blockIdx.x);
   if (tid == 0) {
-    run->count = static_cast<int>(min(per, total - first));
+    run->count = static_cast<int>(min(per, left - first));
     run->per = static_cast<int>(per);
   }
-  if (first >= base && first < base + mine) {
-    long long rem = first - base;
+  if (first >= base && first - base < mine) {
+    U rem = first - base;
     int b = b0;
     for (; chunk > 1; ++b) {  // (a thread with one sequence still holds it)
-      const long long u = units_of(b, false);
+      const U u = units_of(b, false);
       if (rem < u) break;
       rem -= u;
     }
@@ -129,7 +128,7 @@ __device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun* run, Uni
   }
 }
 
-// Part of one tile's key blocks: blocks [j0, j1) of `blocks`. The tile's first
+// Part of one item's key blocks: blocks [j0, j1) of `blocks`. The item's first
 // and last blocks lie in CTAs first_cta and last_cta, its first unit is unit
 // `lead` of first_cta's run. j1 < 0 ends a run.
 struct Segment {
@@ -139,9 +138,10 @@ struct Segment {
 };
 static_assert(sizeof(Segment) == 48, "three int4");
 
-// The first block of the tile that the p-th CTA after first_cta works on.
-__device__ __forceinline__ int part_begin(const Segment& s, int p, int per, int weight) {
-  return p == 0 ? 0 : static_cast<int>((static_cast<long long>(p) * per - s.lead + weight - 1) / weight);
+// The first block of the item that the p-th CTA after first_cta works on, with
+// 2^shift units to a block.
+__device__ __forceinline__ int part_begin(const Segment& s, int p, int per, int shift) {
+  return p == 0 ? 0 : static_cast<int>((static_cast<long long>(p) * per - s.lead + (1 << shift) - 1) >> shift);
 }
 
 __device__ __forceinline__ Segment end_segment() {
@@ -205,18 +205,20 @@ __device__ __forceinline__ void seg_release(SegRing& r, uint32_t& st, uint32_t& 
 // following 32 entries, the next sequence's first 32 entries) are loaded long
 // before they are needed, so that only the run's first block waits for them.
 //
-// Tiles: items(s), blocks(s, tile), a block's weight(s, tile) and before(s, k)
-// (the units of tiles 0 .. k - 1) of one key/value head of a sequence with new
-// tokens.
-template <typename Tiles>
+// Tiles: items(s), blocks(s, item), shift(s, item) (log2 of the units in a block)
+// and before<U>(s, k) (the units of items 0 .. k - 1) of one key/value head of a
+// sequence with new tokens.
+// (The code is laid out so that each step of it exists once: the walk is a few
+// hundred instructions that two warps run, and copies of it slowed short texts.)
+template <typename U, typename Tiles>
 struct RunWalker {
   const PagedAttend& a;
   const Tiles& tiles;
   const int lane, per, count;
-  int pos;     // units of the run up to the current segment's end
-  bool alive;  // there is a current segment
+  int pos;  // where the current item ends, counted from the run's first unit
   Segment seg;
   SeqInfo s, next_s;
+  U rem;    // before the first segment: where the run starts in its sequence
   int items, next_b;
   int seq_base;
   SeqWords seq_cur, seq_ahead;
@@ -261,10 +263,11 @@ struct RunWalker {
     items = tiles.items(s);
   }
 
-  __device__ __forceinline__ RunWalker(const PagedAttend& args, const Tiles& t, const PlanRun& run, int ln)
-      : a(args), tiles(t), lane(ln), per(run.per), count(run.count), pos(0), alive(run.count > 0) {
-    if (!alive) return;
+  __device__ __forceinline__ RunWalker(const PagedAttend& args, const Tiles& t, const PlanRun<U>& run, int ln)
+      : a(args), tiles(t), lane(ln), per(run.per), count(run.count), pos(0) {
+    if (count <= 0) return;
     s = run.s;
+    rem = run.rem;
     seg = Segment{};
     seg.b = run.b;
     enter();
@@ -272,71 +275,86 @@ struct RunWalker {
     seq_base = seg.b;
     seq_cur = seq_load(a, seq_base + lane);
     seq_ahead = seq_load(a, seq_base + 32 + lane);
-    next_b = -1;  // looked for when the run's first loads are on their way
-    const long long each = tiles.before(s, items);
-    seg.head = static_cast<int>(fast_div(run.rem, each));
-    const long long rem = run.rem - seg.head * each;
-    // The last tile with before(tile) <= rem, 32 candidates at a time.
+    next_b = -1;  // not looked for yet
+  }
+
+  // The run's first block: unit `rem` of the sequence, or the next block's start.
+  __device__ __forceinline__ void find() {
+    const U each = tiles.template before<U>(s, items);
+    seg.head = static_cast<int>(rem / each);
+    rem -= seg.head * each;
+    // The last item with before(item) <= rem, 32 candidates at a time.
     for (int width = items; width > 1;) {
       const int step = (width + 31) / 32;
-      const unsigned below =
-          __ballot_sync(0xffffffffu, lane * step < width && tiles.before(s, seg.tile + lane * step) <= rem);
+      const unsigned below = __ballot_sync(
+          0xffffffffu, lane * step < width && tiles.template before<U>(s, seg.tile + lane * step) <= rem);
       const int l = 31 - __clz(below);
       seg.tile += l * step;
       width = min(step, width - l * step);
     }
     seg.blocks = tiles.blocks(s, seg.tile);
-    const int weight = tiles.weight(s, seg.tile), off = static_cast<int>(rem - tiles.before(s, seg.tile));
-    seg.j0 = (off + weight - 1) / weight;
-    pos = seg.j0 * weight - off;
-    if (seg.j0 == seg.blocks) alive = step_tile();  // the run starts inside the tile's last block
-    else open();
+    const int shift = tiles.shift(s, seg.tile);
+    const int off = static_cast<int>(rem - tiles.template before<U>(s, seg.tile));
+    seg.j0 = (off + (1 << shift) - 1) >> shift;
+    pos = ((seg.j0 < seg.blocks ? seg.j0 : seg.blocks) << shift) - off;
   }
 
-  // The segment that starts at seg.j0, unit `pos` of the run. A tile that began
-  // before it began in the run (only a run's first can); one that does not end
-  // in it is its last.
-  __device__ __forceinline__ void open() {
-    const int me = blockIdx.x, weight = tiles.weight(s, seg.tile);
-    const int len = min((count - pos + weight - 1) / weight, seg.blocks - seg.j0);
-    const int begin = pos - seg.j0 * weight;  // where the tile begins, counted from the run's first unit
+  // On to the run's next segment (its first, at the first call); false at the end.
+  __device__ __forceinline__ bool advance() {
+    bool step = true;
+    if (pos == 0) {  // (later on an item has ended past the run's first unit)
+      if (count <= 0) return false;
+      find();
+      step = seg.j0 >= seg.blocks;  // the run starts inside the item's last block
+    }
+    if (step) {
+      if (pos >= count) return false;
+      seg.j0 = 0;
+      if (++seg.tile == items) {
+        seg.tile = 0;
+        if (++seg.head == a.Hkv) {  // the next sequence
+          seg.head = 0;
+          if (next_b < 0) look_ahead(seg.b);
+          if (next_b >= a.B) return false;
+          s = next_s;
+          seg.b = next_b;
+          first = next_first;
+          next_b = -1;
+          enter();
+        }
+      }
+      seg.blocks = tiles.blocks(s, seg.tile);
+    }
+    // The segment that starts at seg.j0, unit `pos` of the run. An item that began
+    // before it began in the run (only a run's first can); one that does not end
+    // in it is its last.
+    const int me = blockIdx.x, shift = tiles.shift(s, seg.tile);
+    const int len = min((count - pos + (1 << shift) - 1) >> shift, seg.blocks - seg.j0);
+    const int begin = pos - (seg.j0 << shift);  // where the item begins, counted from the run's first unit
     seg.j1 = seg.j0 + len;
-    seg.first_cta = me;
+    seg.first_cta = seg.last_cta = me;
     seg.lead = begin;
     if (begin < 0) {
-      const int back = (per - 1 - begin) / per;
+      const int back = static_cast<int>(static_cast<unsigned>(per - 1 - begin) / static_cast<unsigned>(per));
       seg.first_cta = me - back;
       seg.lead = back * per + begin;
     }
-    seg.last_cta = seg.j1 == seg.blocks ? me : me + (begin + (seg.blocks - 1) * weight) / per;
-    pos += len * weight;
+    if (seg.j1 < seg.blocks)
+      seg.last_cta += static_cast<int>(static_cast<unsigned>(begin + ((seg.blocks - 1) << shift)) / static_cast<unsigned>(per));
+    pos = begin + (seg.blocks << shift);  // (past the run's end where the item goes on)
     window = ((seg.j0 * kKeyBlock) >> a.page_shift) & ~31;
     cur = window == 0 ? first : entry(row, pages, window);
     ahead = entry(row, pages, window + 32);
-  }
-
-  // On to the next tile; false at the run's end.
-  __device__ __forceinline__ bool step_tile() {
-    if (pos >= count) return false;
-    seg.j0 = 0;
-    if (next_b < 0) look_ahead(seg.b);
-    if (++seg.tile == items) {
-      seg.tile = 0;
-      if (++seg.head == a.Hkv) {  // the next sequence
-        seg.head = 0;
-        if (next_b >= a.B) return false;
-        s = next_s;
-        seg.b = next_b;
-        first = next_first;
-        enter();
-        look_ahead(seg.b);
-      }
-    }
-    seg.blocks = tiles.blocks(s, seg.tile);
-    open();
     return true;
   }
-  __device__ __forceinline__ void next() { alive = step_tile(); }
+
+  // After a segment's first loads: look for the sequence after this one while
+  // they are on their way.
+  __device__ __forceinline__ void prefetch() {
+    if (next_b < 0 && pos < count) look_ahead(seg.b);
+  }
+
+  __device__ __forceinline__ int box_shift() const { return min(a.page_shift, 7); }
 
   // Where box `box` (of rb keys) of block j lies: the slice (page * Hkv + head)
   // and *r, the row in it. A bad page (reported where `used`) lies past the last
@@ -353,6 +371,49 @@ struct RunWalker {
     if (page >= 0 && page < a.num_pages) return page * a.Hkv + seg.head;
     if (used) raise_invalid(a.ws, 203);
     return a.num_pages * a.Hkv;
+  }
+};
+
+// A ring of K or of V tiles (128 keys of one head, D columns as D / 64 boxes
+// columns) and the producer warp that fills it. K and V have a warp each: a lane's
+// box takes about 75 cycles to issue, one after the other, and with small
+// pages a block has up to 32 of them (draft tokens over 32-key pages at D = 64:
+// 1400 cycles a block with one warp for both, the limit there).
+template <int D>
+struct TileRing {
+  static constexpr int CH = D / 64, kBox = kKeyBlock * 128, kTile = CH * kBox;
+  const CUtensorMap* map;
+  uint8_t* tiles;
+  uint64_t *full, *empty;
+  uint32_t slots;
+  int rb;  // keys per box: a page, or 128 of a larger one
+  uint32_t st, ph, loads;
+
+  // Load block j of the walk's segment (the whole warp).
+  template <typename Walk>
+  __device__ __forceinline__ bool load(Walk& walk, int j, int lane, volatile int* abort_flag, int* ws, int site) {
+    const int boxes = (min(kKeyBlock, walk.seg.n - j * kKeyBlock) + rb - 1) >> walk.box_shift();  // 0 for a sequence without keys
+    int row;
+    const int z = walk.locate(j, lane / CH, rb, lane / CH < boxes, &row);
+    if (!warp_wait(&empty[st], ph ^ 1, abort_flag, ws, site)) return false;
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * rb * 128 * CH);
+    __syncwarp();
+    if (lane < boxes * CH)
+      tma_load_3d(tiles + st * kTile + (lane % CH) * kBox + (lane / CH) * rb * 128, map, &full[st], (lane % CH) * 64, row,
+                  z);
+    __syncwarp();
+    ++loads;
+    if (++st == slots) { st = 0; ph ^= 1; }
+    return true;
+  }
+
+  // An aborting producer lets its copies in flight land before the CTA exits.
+  __device__ __forceinline__ void settle() const {
+    int never = 0;
+    for (uint32_t s = 0; s < slots && s < loads; ++s) {
+      const uint32_t idx = loads - 1 - s;
+      mbar_wait(&full[idx % slots], (idx / slots) & 1, &never, nullptr, 0);
+    }
   }
 };
 

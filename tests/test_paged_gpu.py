@@ -572,6 +572,23 @@ def test_attend_any_earlier_workspace_use():
         b.check(o, True)
 
 
+@pytest.mark.parametrize("m, Hkv", [(1, 256), (65, 128)])
+def test_attend_wide_tables(m, Hkv):
+    """Tables so wide that the call's units of work may need 64 bits (64
+    sequences of up to 2^24 tokens, few of them there)."""
+    kv = [m + 7 * i for i in range(63)] + [m + 700]
+    b = Batch([m] * 64, kv, Hkv, Hkv, 64, 16, seed=m)
+    wide = torch.full((64, 1 << 20), -1, dtype=torch.int32, device=DEV)
+    wide[:, :b.table.shape[1]] = b.table
+    narrow, o1 = b.table, b.run(True)
+    b.table = wide
+    o2 = b.run(True)
+    b.fine()
+    assert torch.equal(o1, o2)
+    b.table = narrow
+    b.check(o2, True)
+
+
 def test_attend_matches_packed_forward():
     """Without earlier tokens and without the mask it is sigattn_fwd_varlen."""
     lens = [300, 1, 129, 64]
