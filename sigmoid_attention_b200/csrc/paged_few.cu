@@ -217,10 +217,10 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
         if (!(ok = seg_read<false>(bar.ring, rst, rph, &seg, abort_flag, ws, 310))) break;
         seg_release(bar.ring, rst, rph, true);
         if (seg.j1 < 0) break;
-        if (!(ok = mbar_wait(&bar.q_full[qb], qph, abort_flag, ws, 311))) break;
+        if (!(ok = role_wait(&bar.q_full[qb], qph, abort_flag, ws, 311))) break;
         for (int j = seg.j0; j < seg.j1; ++j) {
-          if (!(ok = mbar_wait(&bar.full[st], ph, abort_flag, ws, 312))) break;
-          if (!(ok = mbar_wait(&bar.s_empty[sb], sph ^ 1, abort_flag, ws, 313))) break;
+          if (!(ok = role_wait(&bar.full[st], ph, abort_flag, ws, 312))) break;
+          if (!(ok = role_wait(&bar.s_empty[sb], sph ^ 1, abort_flag, ws, 313))) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)

@@ -311,12 +311,12 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         // one: the other issuer's products must have completed. (No issuer gets
         // four segments ahead of the other: the K ring is shorter.)
         if (segs > 0 && (t == 0 ? was_two && !sh.two : sh.two && !was_two) &&
-            !(ok = mbar_wait(&bar.fin[1 - t][(segs - 1) & 3], ((segs - 1) >> 2) & 1, abort_flag, ws, 417)))
+            !(ok = role_wait(&bar.fin[1 - t][(segs - 1) & 3], ((segs - 1) >> 2) & 1, abort_flag, ws, 417)))
           break;
         uint64_t q_tile = 0;  // this side's query tile (dual: the only one)
         uint64_t* q_free = nullptr;
         for (int x = 0; x <= (sh.two ? 1 : 0); ++x) {
-          if (!(ok = mbar_wait(&bar.q_full[qst], qph, abort_flag, ws, 411))) break;
+          if (!(ok = role_wait(&bar.q_full[qst], qph, abort_flag, ws, 411))) break;
           if (x == t) {
             q_tile = d_q + qst * kTile;
             q_free = &bar.q_empty[qst];
@@ -330,11 +330,11 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         // The side that block j works on here, or -1.
         auto side_of = [&](int j) { return sh.dual ? (t == 0 ? (j - seg.j0) & 1 : -1) : (j < end ? t : -1); };
         auto take_k = [&](int j) -> bool {
-          if (!mbar_wait(&bar.k_full[kst], kph, abort_flag, ws, 412)) return false;
+          if (!role_wait(&bar.k_full[kst], kph, abort_flag, ws, 412)) return false;
           const int e = side_of(j);
           if (e >= 0) {
             // SEP_P: the epilogue must have copied the side's previous S out.
-            if (C::SEP_P && (any >> e & 1) && !mbar_wait(&bar.s_read[e], (odd >> e & 1) ^ 1, abort_flag, ws, 413)) return false;
+            if (C::SEP_P && (any >> e & 1) && !role_wait(&bar.s_read[e], (odd >> e & 1) ^ 1, abort_flag, ws, 413)) return false;
             odd ^= 1u << e;
             any |= 1u << e;
             tc_fence_after();
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         };
         uint32_t podd = odd;  // parity of the side's blocks before the one whose P is taken next
         auto take_v = [&](int j) -> bool {
-          if (!mbar_wait(&bar.v_full[vst], vph, abort_flag, ws, 414)) return false;
+          if (!role_wait(&bar.v_full[vst], vph, abort_flag, ws, 414)) return false;
           const int e = side_of(j);
           if (e >= 0) {
             // The products take keys in sixteens: rows of V past the text's end in
@@ -371,9 +371,9 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
             const uint32_t tm_p = tmem + (C::SEP_P ? C::TM_P + e * 64 : C::TM_S + e * 128);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              if (!mbar_wait(&bar.p_full[2 * e + h], podd >> e & 1, abort_flag, ws, 415)) return false;
+              if (!role_wait(&bar.p_full[2 * e + h], podd >> e & 1, abort_flag, ws, 415)) return false;
               if (fresh == 0 && h == 0) {
-                if (!mbar_wait(&bar.o_empty[t], oph ^ 1, abort_flag, ws, 416)) return false;
+                if (!role_wait(&bar.o_empty[t], oph ^ 1, abort_flag, ws, 416)) return false;
                 oph ^= 1;
               }
               tc_fence_after();

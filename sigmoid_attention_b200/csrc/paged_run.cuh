@@ -26,10 +26,19 @@ constexpr int kKeyBlock = 128;
 // are written as zeros).
 __device__ __forceinline__ int seq_blocks(int n) { return n > 0 ? (n + kKeyBlock - 1) / kKeyBlock : 1; }
 
+// mbar_wait with its slow path out of line: inlined at every wait, the clock and
+// abort code made the roles' loops too long for the instruction cache.
+static __device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* ws, int site) {
+  return mbar_wait(bar, parity, abort_flag, ws, site);
+}
+__device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* ws, int site) {
+  return mbar_try_wait(bar, parity) || wait_longer(bar, parity, abort_flag, ws, site);
+}
+
 // A wait by a whole warp: every lane gets the same answer, so that an aborting
 // warp leaves its loop as one.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* ws, int site) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, ws, site));
+  return __all_sync(0xffffffffu, role_wait(bar, parity, abort_flag, ws, site));
 }
 
 // (The lengths and tables below are loaded from L2: the kernel before this one
@@ -188,7 +197,7 @@ __device__ __forceinline__ Segment seg_peek(SegRing& r, uint32_t st) {
 template <bool WARP>
 __device__ __forceinline__ bool seg_read(SegRing& r, uint32_t st, uint32_t ph, Segment* s, volatile int* abort_flag,
                                          int* ws, int site) {
-  if (!(WARP ? warp_wait(&r.full[st], ph, abort_flag, ws, site) : mbar_wait(&r.full[st], ph, abort_flag, ws, site)))
+  if (!(WARP ? warp_wait(&r.full[st], ph, abort_flag, ws, site) : role_wait(&r.full[st], ph, abort_flag, ws, site)))
     return false;
   *s = seg_peek(r, st);
   return true;
