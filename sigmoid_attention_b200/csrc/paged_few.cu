@@ -404,9 +404,38 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     // The sum of a tile's parts, by the output warps: `rows` rows of D, four at a
     // time. Lanes take four columns each, so a warp reads SUB rows of a part at
     // once; part p belongs to slice p % SLICES, the slices are added in order.
+    // (Up to 16 parts, each thread adds its columns itself, eight loads at a time:
+    // no exchange through shared memory.)
     auto join = [&](const Segment& seg, int rows) -> bool {
       constexpr int LPR = C::LPR, SLICES = C::SLICES, RC = C::RC, UNROLL = 3;
       const int np = seg.last_cta - seg.first_cta + 1;
+      if (np <= 16) {
+        for (int e = ow * 32 + lane; e < rows * LPR; e += C::OUT_WARPS * 32) {
+          const float* part = a.parts + static_cast<size_t>(2 * seg.first_cta + 1) * (NR * D) + 4 * e;
+          float4 sum = __ldcg(reinterpret_cast<const float4*>(part));
+          part += NR * D;
+#pragma unroll 1
+          for (int p0 = 1; p0 < np; p0 += 8, part += 16 * (NR * D)) {
+            float4 x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (p0 + u < np) x[u] = __ldcg(reinterpret_cast<const float4*>(part + 2 * u * (NR * D)));
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              sum.x += x[u].x;
+              sum.y += x[u].y;
+              sum.z += x[u].z;
+              sum.w += x[u].w;
+            }
+          }
+          const int n = e / LPR;
+          *reinterpret_cast<uint2*>(a.o + (static_cast<size_t>(seg.start + n / G) * a.Hq + seg.head * G + n % G) * D +
+                                    4 * (e % LPR)) = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+        }
+        return true;
+      }
       const int slice = ow * C::SUB + lane / LPR, l4 = lane % LPR;
       float4* red = reinterpret_cast<float4*>(smem + C::OFF_RED);
       for (int n0 = 0; n0 < rows; n0 += RC) {
