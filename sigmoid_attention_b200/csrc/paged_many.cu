@@ -13,7 +13,7 @@
 //  * Keys come from pages: the producer warp looks the page numbers up and its
 //    lanes issue one box per page and 64 columns.
 //  * Each row has its own N (causal): the bias is a register of the row's
-//    thread, and only blocks past the tile's first row's N run masking code.
+//    thread, and only blocks past the tile's first row's N are masked.
 //    A tile stops at the last block that one of its rows sees.
 //  * The work is shared out in equal runs of key blocks (paged_run.cuh): few
 //    tiles over long texts are cut along the keys, and the causal triangle's
@@ -148,6 +148,43 @@ struct TileMath {
     return sum + 2 * (static_cast<U>(none) + floor_sum<U>(k - none, item, c + (none + 1) * item + kKeyBlock - 1));
   }
 };
+
+// The bf16 weights of 32 scores of one thread: sigma(x) for y = x log2(e) =
+// s scale_l2e + neg_log2n. As in the whole-sequence kernels (sigmoid_n) a warp
+// whose scores all lie in the far tail takes one exponential per weight. The
+// general form here is 1 / (1 + 2^-y), one more MUFU operation where theirs is a
+// polynomial: half the instructions, and instructions are what the short texts
+// that come here wait for (eight sequences of 512 tokens: 82 -> 58 us); also exact
+// to about 1e-7 instead of 9e-4.
+__device__ __forceinline__ void weights32(const uint32_t (&s)[32], float scale_l2e, float neg_log2n, bool lane_ok,
+                                          uint32_t (&pk)[16]) {
+  const uint64_t c1 = f2_splat(scale_l2e), c0 = f2_splat(neg_log2n - kTailY);
+  uint64_t z[16];  // y - kTailY
+  uint32_t all = 0xffffffffu;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    z[e] = f2_fma(f2_pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c1, c0);
+    all &= static_cast<uint32_t>(z[e]) & static_cast<uint32_t>(z[e] >> 32);
+  }
+  if (__all_sync(0xffffffffu, (all >> 31) != 0 || !lane_ok)) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float2 zz = f2_unpack(z[e]);
+      const uint64_t w = f2_pack(ex2_approx(zz.x), ex2_approx(zz.y));
+      const uint64_t t = f2_fma(f2_fma(w, f2_splat(kTailC * kTailC * kTailC), f2_splat(-kTailC * kTailC)), w, f2_splat(kTailC));
+      const float2 q = f2_unpack(f2_mul(t, w));
+      pk[e] = pack_bf16x2(q.x, q.y);
+    }
+  } else {
+    constexpr float k = 16.0f;  // 2^-kTailY
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float2 zz = f2_unpack(z[e]);
+      const float2 d = f2_unpack(f2_fma(f2_pack(ex2_approx(-zz.x), ex2_approx(-zz.y)), f2_splat(k), f2_splat(1.0f)));
+      pk[e] = pack_bf16x2(rcp_approx(d.x), rcp_approx(d.y));
+    }
+  }
+}
 
 // Where a segment's parts differ by its tiles. Two tiles: each works on the blocks
 // that its rows see. One tile: "dual" from two blocks on, both sides take blocks
@@ -458,9 +495,17 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
       // Warps whose rows are all past the tile's last leave S and P alone
       // (what their rows of P hold reaches no other row).
       const bool idle = __all_sync(0xffffffffu, !row_ok);
-      // One pass over key block j; the rows' masks only in MASKED passes.
-      auto pass = [&](const int j, auto masked) -> bool {
-        constexpr bool MASKED = decltype(masked)::value;
+      const int plain = min(end, clear / kKeyBlock);  // blocks that every row sees whole
+      // One pass over key block j. How often this code exists decides how short
+      // texts run, whose passes wait for instructions (the forward kernel's
+      // instances for masked and unmasked blocks with both chunks unrolled: 4500
+      // cycles for a chunk instead of 800). At d = 128 one copy serves both chunks
+      // and masked blocks too (kEither); at d = 64, where the passes set the pace,
+      // masked blocks have a copy of their own and the chunks are unrolled
+      // (4096-token prompts: 133 us, with one copy 154 us).
+      enum : int { kPlain, kMasked, kEither };
+      auto pass = [&](const int j, auto mode) -> bool {
+        constexpr int MODE = decltype(mode)::value;
         if (!warp_wait(&bar.s_full[t], (bits & kS) != 0, abort_flag, ws, 421)) return false;
         bits ^= kS;
         // d = 128: the tiles take turns over the blocks that both work on (tile 1
@@ -475,7 +520,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         }
         tc_fence_after();
         if (!idle) {
-#pragma unroll
+#pragma unroll (C::SEP_P ? 2 : 1)
           for (int c = 0; c < 2; ++c) {
             uint32_t s[32];
             tmem_ld32(tS + 32 * c, s);
@@ -484,12 +529,17 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
               __syncwarp();
               if (lane == 0) mbar_arrive(&bar.s_read[t]);
             }
-            uint32_t pk[16];
-            if constexpr (MASKED) mask_scores(s, seen - (j * kKeyBlock + h * 64 + 32 * c), true);
-            sigmoid32<false>(s, scale_l2e, neg_log2n, nullptr, row_ok);
+            if (MODE == kMasked || (MODE == kEither && j >= plain)) {
+              // One bit per key: tests of a word's bits go to predicates several at a
+              // time, where 32 comparisons with `seen` take one instruction each.
+              const int left = seen - (j * kKeyBlock + h * 64 + 32 * c);
+              const uint32_t keep = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              pk[e] = pack_bf16x2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+              for (int e = 0; e < 32; ++e)
+                if (!(keep & (1u << e))) s[e] = 0xff800000u;  // -inf: weight 0
+            }
+            uint32_t pk[16];
+            weights32(s, scale_l2e, neg_log2n, row_ok, pk);
             // SEP_P: the P region is free once the tile's previous PV completed.
             if (C::SEP_P && c == 0 && (bits & kPending)) {
               if (!warp_wait(&bar.pv_done[t], (bits & kPv) != 0, abort_flag, ws, 423)) return false;
@@ -515,9 +565,12 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         }
         return true;
       };
-      const int plain = min(end, clear / kKeyBlock);  // blocks that every row sees whole
-      for (; ok && j < plain; j += step) ok = pass(j, std::false_type{});
-      for (; ok && j < end; j += step) ok = pass(j, std::true_type{});
+      if constexpr (C::SEP_P) {
+        for (; ok && j < plain; j += step) ok = pass(j, std::integral_constant<int, kPlain>{});
+        for (; ok && j < end; j += step) ok = pass(j, std::integral_constant<int, kMasked>{});
+      } else {
+        for (; ok && j < end; j += step) ok = pass(j, std::integral_constant<int, kEither>{});
+      }
       if (!ok) break;
 
       // The segment again, from the ring (its slot is released only below, so
