@@ -50,12 +50,18 @@ struct PagedAttend {
   const int *cu, *kv, *table;
   int B, Hq, Hkv, max_q, total, max_pages, page_shift, num_pages, d, causal;
   int least;     // fewest units of work in a CTA's run (paged_run.cuh)
+  float cut;     // what a row of a part costs to add up, in units of work
   float* parts;  // partial sums of tiles cut over CTAs, two places per CTA
   int* ws;
 };
 
 // CTAs of a paged attention call at most (the workspace holds two parts each).
 constexpr int kMaxPagedCtas = 152;
+// PagedAttend::cut. Measured, per setting 0 / kFewCut / 5 kFewCut: one token of 8
+// query rows over 36663 keys 25.7 / 16.4 / 19.1 us, of 16 over 131072 52.4 / 36.3 /
+// 44.5 us; and 0 / 2/3 kManyCut / 3 kManyCut: 34 tokens of 7 heads over 29856 keys
+// 84 / 41 / 56 us, 200 tokens of 8 heads over 4000 keys 51 / 37 / 43 us.
+constexpr float kFewCut = 0.02f, kManyCut = 0.003f;
 // Query rows per key/value head (G * new tokens) up to which paged_few.cu serves.
 constexpr int kFewRows = 64;
 

@@ -159,14 +159,15 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
   for (int i = threadIdx.x; i < 2 * C::Q_BYTES / 16; i += C::THREADS)
     reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
+  const int G = a.Hq / a.Hkv;
   grid_dep_launch();
   grid_dep_wait();
-  plan_run<C::THREADS>(a, &bar.run, [](const SeqInfo& s) -> U { return seq_blocks(s.n); });
+  plan_run<C::THREADS>(a, &bar.run, [](const SeqInfo& s) -> U { return seq_blocks(s.n); },
+                       [&](const SeqInfo& s) { return a.cut * static_cast<float>(s.m * G) * seq_blocks(s.n); });
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem_base;
-  const int G = a.Hq / a.Hkv;
 
   if (warp == kLoadK || warp == kLoadV) {
     // ------------------------------------- producers: segments, Q and K; V

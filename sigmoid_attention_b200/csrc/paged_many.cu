@@ -255,7 +255,11 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
   const TileMath math{T, a.causal};
   grid_dep_launch();
   grid_dep_wait();
-  plan_run<C::THREADS>(a, &bar.run, [&](const SeqInfo& s) { return math.before<U>(s, math.items(s)); });
+  plan_run<C::THREADS>(a, &bar.run, [&](const SeqInfo& s) { return math.before<U>(s, math.items(s)); },
+                       [&](const SeqInfo& s) {
+                         const float tiles = math.two(s, 0) ? 2.0f : 1.0f;
+                         return a.cut * tiles * tiles * static_cast<float>(min(s.m, 2 * T) * G) * seq_blocks(s.n);
+                       });
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -78,12 +78,18 @@ struct PlanRun {
 // at least a.least units long (at least a block's, so that a tile's CTAs all
 // have a block of it). U: an unsigned type that holds the call's units; the
 // usual 32 bits make this half as long as 64.
+// join(s): how long the parts of the sequence's largest tile take to add up, if
+// cut at every unit, in units of work. A tile of b units cut into runs of x
+// takes about x + join(s) / x, least at x = sqrt(join): runs are that long at
+// least, so that few tiles over long texts are not cut into more parts than
+// their last CTA can add up in the time the cut saves.
 // Ends before the caller's next barrier; every thread of the CTA takes part.
-template <int THREADS, typename U, typename Units>
-__device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun<U>* run, Units units) {
+template <int THREADS, typename U, typename Units, typename Join>
+__device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun<U>* run, Units units, Join join) {
   constexpr int kWarps = THREADS / 32;
   static_assert(THREADS % 32 == 0 && kWarps <= 32, "whole warps");
   __shared__ U sums[kWarps];
+  __shared__ unsigned joins[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int chunk = ceil_div(a.B, THREADS);
   const int b0 = min(a.B, tid * chunk), b1 = min(a.B, b0 + chunk);
@@ -96,7 +102,14 @@ __device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun<U>* run, 
     return s.m > 0 ? units(s) * static_cast<U>(a.Hkv) : 0;
   };
   U mine = 0;
-  for (int b = b0; b < b1; ++b) mine += units_of(b, true);
+  float longest = 0.f;
+  for (int b = b0; b < b1; ++b) {
+    const U u = units_of(b, true);
+    mine += u;
+    if (u > 0) longest = fmaxf(longest, join(s));
+  }
+  // (nonnegative floats order like their bits)
+  const unsigned most = __reduce_max_sync(0xffffffffu, __float_as_uint(longest));
   auto scan = [&](U v) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -106,13 +119,17 @@ __device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun<U>* run, 
     return v;
   };
   const U incl = scan(mine);
-  if (lane == 31) sums[warp] = incl;
+  if (lane == 31) {
+    sums[warp] = incl;
+    joins[warp] = most;
+  }
   __syncthreads();
   const U upto = scan(lane < kWarps ? sums[lane] : 0);
   const U total = __shfl_sync(0xffffffffu, upto, kWarps - 1);
   const U before = __shfl_sync(0xffffffffu, upto, warp > 0 ? warp - 1 : 0);
   const U base = (warp > 0 ? before : 0) + incl - mine;
-  U per = max(static_cast<U>(a.least), (total + gridDim.x - 1) / gridDim.x);
+  const float all_join = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < kWarps ? joins[lane] : 0));
+  U per = max(static_cast<U>(sqrtf(all_join)), max(static_cast<U>(a.least), (total + gridDim.x - 1) / gridDim.x));
   U left = total;
   if (per > INT_MAX) {  // beyond any call that could end
     if (blockIdx.x == 0 && tid == 0) raise_invalid(a.ws, 206);
