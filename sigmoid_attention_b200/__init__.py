@@ -136,8 +136,15 @@ def _check(fn: str, status: int) -> None:
         raise err
 
 
+# The current stream's handle without a Stream object around it (0.1 instead of
+# 3 us), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_ptr(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
@@ -316,79 +323,89 @@ def sigattn_bwd_dkdv_varlen(q, k, v, dout, dk, dv, cu_seqlens, max_seqlen: int, 
 # ---------------------------------------------------------------------------
 # Serving from a paged cache (see the C header for the conventions)
 # ---------------------------------------------------------------------------
-def _rows(t: torch.Tensor, name: str, heads: int = 0, d: int = 0) -> int:
-    """Pointer of a [rows, heads, d] bf16 tensor whose rows may be strided
-    (slices of one fused projection)."""
-    if t.dim() != 3 or not t.is_cuda or t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be a [rows, heads, d] CUDA torch.bfloat16 tensor")
-    if (t.stride(2) != 1 and t.shape[2] > 1) or (t.stride(1) != t.shape[2] and t.shape[1] > 1):
-        raise ValueError(f"{name} must be contiguous within each row")
-    if (heads and t.shape[1] != heads) or (d and t.shape[2] != d):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [rows, {heads or t.shape[1]}, {d or t.shape[2]}]")
+# These checks run before every single-token call, whose kernels take a few
+# microseconds: each is one cheap comparison, and says what is wrong elsewhere.
+_i32, _bf16, _u8 = torch.int32, torch.bfloat16, torch.uint8
+
+
+def _refuse(t, name: str, dtype, dev: int, count=None):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected the current device cuda:{dev}")
+    if t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
+    raise ValueError(f"{name} has {t.numel()} elements, expected {count}")
+
+
+def _arg(t, name: str, dtype, dev: int) -> int:
+    """Pointer of a contiguous tensor on the device `dev`, which is the current
+    one (the library launches on it)."""
+    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
+        _refuse(t, name, dtype, dev)
     return t.data_ptr()
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _ints(t, name: str, count: int, dev: int) -> int:
+    """The same for `count` int32 values."""
+    if t.get_device() != dev or t.dtype is not _i32 or t.numel() != count or not t.is_contiguous():
+        _refuse(t, name, _i32, dev, count)
+    return t.data_ptr()
 
 
-def _same_device(first: torch.Tensor, **others) -> None:
-    """All tensors on one device, which must be the current one (the library
-    launches on the current device)."""
-    if first.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {first.device}, the current device is cuda:{torch.cuda.current_device()}")
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+def _rows(t, name: str, rows: int, heads: int, d: int, dev: int):
+    """Pointer and row stride of [rows, heads, d] bf16 values whose rows may be
+    strided (slices of one fused projection)."""
+    if t.get_device() != dev:
+        _refuse(t, name, _bf16, dev)
+    if t.dtype is not _bf16 or tuple(t.shape) != (rows, heads, d):
+        raise ValueError(f"{name} must be a [{rows}, {heads}, {d}] CUDA torch.bfloat16 tensor, got {tuple(t.shape)} {t.dtype}")
+    s, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and heads > 1):
+        raise ValueError(f"{name} must be contiguous within each row")
+    return t.data_ptr(), s if rows > 1 else heads * d
 
 
-def _int32(t: torch.Tensor, name: str, *shape: int) -> int:
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    return _dev(t, name, torch.int32)
-
-
-def _cache_dims(k_cache: torch.Tensor, v_cache: torch.Tensor):
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+def _cache(k_cache, v_cache, dev: int):
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [num_pages, Hkv, page_size, d] tensors of one shape")
-    return tuple(k_cache.shape)
+    return _arg(k_cache, "k_cache", _bf16, dev), _arg(v_cache, "v_cache", _bf16, dev), *shape
+
+
+def _table(t, B: int, dev: int):
+    if t.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    width = t.shape[1]
+    return _ints(t, "block_table", B * width, dev), width
 
 
 def sigattn_paged_reserve(cached_lens, new_lens, block_table, free_pages, free_count, free_count_out, cu_seqlens,
                           kv_lens, slots, positions, page_size: int, workspace, stream=None) -> None:
     """Take pages for new_lens[b] more tokens of every sequence and write
     cu_seqlens, kv_lens, slots and positions (None to omit) for them."""
-    B = cached_lens.numel()
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    _same_device(cached_lens, new_lens=new_lens, block_table=block_table, free_pages=free_pages, free_count=free_count,
-                 free_count_out=free_count_out, cu_seqlens=cu_seqlens, kv_lens=kv_lens, slots=slots,
-                 positions=positions, workspace=workspace)
-    rows = slots.numel()
+    dev = torch.cuda.current_device()
+    B, rows = cached_lens.numel(), slots.numel()
+    table, width = _table(block_table, B, dev)
     _check("sigattn_paged_reserve", library().sigattn_paged_reserve(
-        _int32(cached_lens, "cached_lens", B), _int32(new_lens, "new_lens", B),
-        _int32(block_table, "block_table", B, block_table.shape[1]), _dev(free_pages, "free_pages", torch.int32),
-        _int32(free_count, "free_count", 1), _int32(free_count_out, "free_count_out", 1),
-        _int32(cu_seqlens, "cu_seqlens", B + 1), _int32(kv_lens, "kv_lens", B), _int32(slots, "slots", rows),
-        None if positions is None else _int32(positions, "positions", rows), B, block_table.shape[1], int(page_size),
-        free_pages.numel(), rows, _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream_ptr(stream)))
+        _ints(cached_lens, "cached_lens", B, dev), _ints(new_lens, "new_lens", B, dev), table,
+        _arg(free_pages, "free_pages", _i32, dev), _ints(free_count, "free_count", 1, dev),
+        _ints(free_count_out, "free_count_out", 1, dev), _ints(cu_seqlens, "cu_seqlens", B + 1, dev),
+        _ints(kv_lens, "kv_lens", B, dev), _arg(slots, "slots", _i32, dev),
+        None if positions is None else _ints(positions, "positions", rows, dev), B, width, page_size,
+        free_pages.numel(), rows, _arg(workspace, "workspace", _u8, dev), workspace.numel(), _stream_ptr(stream)))
 
 
 def sigattn_paged_release(kv_lens, keep_lens, block_table, free_pages, free_count, free_count_out, page_size: int,
                           workspace, stream=None) -> None:
     """Push the pages past each sequence's first keep_lens[b] tokens (None: all
     pages) back on the stack of free pages."""
+    dev = torch.cuda.current_device()
     B = kv_lens.numel()
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    _same_device(kv_lens, keep_lens=keep_lens, block_table=block_table, free_pages=free_pages, free_count=free_count,
-                 free_count_out=free_count_out, workspace=workspace)
+    table, width = _table(block_table, B, dev)
     _check("sigattn_paged_release", library().sigattn_paged_release(
-        _int32(kv_lens, "kv_lens", B), None if keep_lens is None else _int32(keep_lens, "keep_lens", B),
-        _int32(block_table, "block_table", B, block_table.shape[1]), _dev(free_pages, "free_pages", torch.int32),
-        _int32(free_count, "free_count", 1), _int32(free_count_out, "free_count_out", 1), B, block_table.shape[1],
-        int(page_size), free_pages.numel(), _dev(workspace, "workspace", torch.uint8), workspace.numel(),
-        _stream_ptr(stream)))
+        _ints(kv_lens, "kv_lens", B, dev), None if keep_lens is None else _ints(keep_lens, "keep_lens", B, dev), table,
+        _arg(free_pages, "free_pages", _i32, dev), _ints(free_count, "free_count", 1, dev),
+        _ints(free_count_out, "free_count_out", 1, dev), B, width, page_size, free_pages.numel(),
+        _arg(workspace, "workspace", _u8, dev), workspace.numel(), _stream_ptr(stream)))
 
 
 def sigattn_paged_write(k, v, slots, k_cache, v_cache, workspace, q=None, q_out=None, positions=None, inv_freq=None,
@@ -397,36 +414,34 @@ def sigattn_paged_write(k, v, slots, k_cache, v_cache, workspace, q=None, q_out=
     (fp32 [pairs]) the keys, and q into q_out, are turned by positions
     (int32 [rows] or [axes, rows]; pair_axis int32 [pairs] names each pair's
     axis)."""
-    pages, Hkv, ps, d = _cache_dims(k_cache, v_cache)
+    dev = torch.cuda.current_device()
+    kc, vc, pages, Hkv, ps, d = _cache(k_cache, v_cache, dev)
     rows = k.shape[0]
-    _same_device(k_cache, v_cache=v_cache, k=k, v=v, slots=slots, workspace=workspace, q=q, q_out=q_out,
-                 positions=positions, inv_freq=inv_freq, pair_axis=pair_axis)
+    kp, ks = _rows(k, "k", rows, Hkv, d, dev)
+    vp, vs = _rows(v, "v", rows, Hkv, d, dev)
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
-    kp, vp = _rows(k, "k", Hkv, d), _rows(v, "v", Hkv, d)
-    if v.shape[0] != rows:
-        raise ValueError("k and v must have the same number of rows")
-    qp = qo = None
-    Hq = qs = qos = 0
+    qp = qo = pp = fp = ap = None
+    Hq = qs = qos = pairs = 0
+    axes = 1
     if q is not None:
         Hq = q.shape[1]
-        qp, qo, qs, qos = _rows(q, "q", Hq, d), _rows(q_out, "q_out", Hq, d), _row_stride(q), _row_stride(q_out)
-        if q.shape[0] != rows or q_out.shape[0] != rows:
-            raise ValueError("q and q_out must have k's number of rows")
-    pp = fp = ap = None
-    pairs, axes = 0, 1
+        qp, qs = _rows(q, "q", rows, Hq, d, dev)
+        qo, qos = _rows(q_out, "q_out", rows, Hq, d, dev)
     if inv_freq is not None:
         if positions is None:
-            raise ValueError("rotary positions need positions and inv_freq")
+            raise ValueError("inv_freq needs positions")
         pairs = inv_freq.numel()
-        fp = _dev(inv_freq, "inv_freq", torch.float32)
-        axes = 1 if positions.dim() == 1 else positions.shape[0]
-        pp = _int32(positions, "positions", *((rows,) if positions.dim() == 1 else (axes, rows)))
-        ap = None if pair_axis is None else _int32(pair_axis, "pair_axis", pairs)
+        fp = _arg(inv_freq, "inv_freq", torch.float32, dev)
+        if positions.dim() > 1:
+            axes = positions.shape[0]
+        pp = _ints(positions, "positions", axes * rows, dev)
+        if pair_axis is not None:
+            ap = _ints(pair_axis, "pair_axis", pairs, dev)
     _check("sigattn_paged_write", library().sigattn_paged_write(
-        kp, _row_stride(k), vp, _row_stride(v), _int32(slots, "slots", rows), _dev(k_cache, "k_cache"),
-        _dev(v_cache, "v_cache"), qp, qs, qo, qos, pp, fp, ap, axes, pairs, int(bool(adjacent)), rows, Hq, Hkv, d, ps,
-        pages, _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream_ptr(stream)))
+        kp, ks, vp, vs, _ints(slots, "slots", rows, dev), kc, vc, qp, qs, qo, qos, pp, fp, ap, axes, pairs,
+        1 if adjacent else 0, rows, Hq, Hkv, d, ps, pages, _arg(workspace, "workspace", _u8, dev), workspace.numel(),
+        _stream_ptr(stream)))
 
 
 def sigattn_paged_workspace_size(Hq: int, Hkv: int, d: int, max_seqlen_q: int) -> int:
@@ -437,22 +452,20 @@ def sigattn_fwd_paged(q, k_cache, v_cache, o, cu_seqlens, kv_lens, block_table, 
                       workspace, stream=None) -> None:
     """Attention of the new tokens' q ([total, Hq, d], rows may be strided) over
     the cached keys and values; o is [total, Hq, d]."""
-    pages, Hkv, ps, d = _cache_dims(k_cache, v_cache)
-    qp = _rows(q, "q", 0, d)
-    total, Hq = q.shape[0], q.shape[1]
-    if tuple(o.shape) != (total, Hq, d):
+    dev = torch.cuda.current_device()
+    kc, vc, pages, Hkv, ps, d = _cache(k_cache, v_cache, dev)
+    if q.dim() != 3:
+        raise ValueError("q must be [total, Hq, d]")
+    total, Hq, _ = q.shape
+    qp, qs = _rows(q, "q", total, Hq, d, dev)
+    if o.shape != q.shape:
         raise ValueError("o must have q's shape")
     B = kv_lens.numel()
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    _same_device(k_cache, v_cache=v_cache, q=q, o=o, cu_seqlens=cu_seqlens, kv_lens=kv_lens, block_table=block_table,
-                 workspace=workspace)
+    table, width = _table(block_table, B, dev)
     _check("sigattn_fwd_paged", library().sigattn_fwd_paged(
-        qp, _row_stride(q), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(o, "o"),
-        _int32(cu_seqlens, "cu_seqlens", B + 1), _int32(kv_lens, "kv_lens", B),
-        _int32(block_table, "block_table", B, block_table.shape[1]), B, Hq, Hkv, int(max_seqlen_q), total,
-        block_table.shape[1], ps, pages, d, int(bool(causal)), _dev(workspace, "workspace", torch.uint8),
-        workspace.numel(), _stream_ptr(stream)))
+        qp, qs, kc, vc, _arg(o, "o", _bf16, dev), _ints(cu_seqlens, "cu_seqlens", B + 1, dev),
+        _ints(kv_lens, "kv_lens", B, dev), table, B, Hq, Hkv, max_seqlen_q, total, width, ps, pages, d,
+        1 if causal else 0, _arg(workspace, "workspace", _u8, dev), workspace.numel(), _stream_ptr(stream)))
 
 
 def sigattn_plan(lengths, B, H, Lmax, d, kind, workspace, stream=None) -> None:
