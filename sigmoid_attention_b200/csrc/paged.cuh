@@ -29,9 +29,6 @@ struct PagedRelease {
   int* ws;
 };
 
-// Cosine/sine entries of one buffer of the write kernel (tokens * pairs).
-constexpr int kWriteTurns = 512;
-
 struct PagedWrite {
   const __nv_bfloat16 *k, *v, *q;
   __nv_bfloat16 *k_cache, *v_cache, *q_out;
@@ -39,7 +36,7 @@ struct PagedWrite {
   const int *slots, *positions, *pair_axis;
   const float* inv_freq;
   int axes, pairs, adjacent, rows, Hq, Hkv, d, page_shift, num_pages;
-  int tokens;  // tokens a CTA takes at a time (set by the launcher)
+  int shares;  // warps per token (set by the launcher)
   int* ws;
 };
 
