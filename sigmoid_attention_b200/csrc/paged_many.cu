@@ -368,12 +368,13 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         }
         if (!ok) break;
         uint32_t fresh = 0;  // 1 once the segment's O holds a product
-        // The side that block j works on here, or -1.
-        auto side_of = [&](int j) { return sh.dual ? (t == 0 ? (j - seg.j0) & 1 : -1) : (j < end ? t : -1); };
-        auto take_k = [&](int j) -> bool {
+        // Block j's K and V. ALT: a dual segment, whose blocks alternate between the
+        // sides; otherwise the side is this issuer's own and its addresses stay
+        // put. `works`: whether it works on the block at all.
+        auto take_k = [&](const int j, auto alt, const bool works) -> bool {
           if (!role_wait(&bar.k_full[kst], kph, abort_flag, ws, 412)) return false;
-          const int e = side_of(j);
-          if (e >= 0) {
+          if (works) {
+            const int e = decltype(alt)::value ? (j - seg.j0) & 1 : t;
             // SEP_P: the epilogue must have copied the side's previous S out.
             if (C::SEP_P && (any >> e & 1) && !role_wait(&bar.s_read[e], (odd >> e & 1) ^ 1, abort_flag, ws, 413)) return false;
             odd ^= 1u << e;
@@ -394,10 +395,10 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
           return true;
         };
         uint32_t podd = odd;  // parity of the side's blocks before the one whose P is taken next
-        auto take_v = [&](int j) -> bool {
+        auto take_v = [&](const int j, auto alt, const bool works) -> bool {
           if (!role_wait(&bar.v_full[vst], vph, abort_flag, ws, 414)) return false;
-          const int e = side_of(j);
-          if (e >= 0) {
+          const int e = decltype(alt)::value ? (j - seg.j0) & 1 : t;
+          if (works) {
             // The products take keys in sixteens: rows of V past the text's end in
             // the last sixteen are zeroed (their weights are 0, and 0 * NaN must
             // not be). Both issuers write the same zeros.
@@ -432,19 +433,30 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
             fresh = 1;
           }
           mma_commit(&bar.v_empty[vst]);
-          if (C::SEP_P && e >= 0) mma_commit(&bar.pv_done[e]);
+          if (C::SEP_P && works) mma_commit(&bar.pv_done[e]);
           if (++vst == C::VST) { vst = 0; vph ^= 1; }
           return true;
         };
-        // S(j + ahead) goes before PV(j) where its region is free of P(j): P has a
-        // region of its own (d = 64), or the next block is the other side's
-        // (dual). Otherwise S(j + 1) overwrites P(j) and follows PV(j).
-        const int ahead = (C::SEP_P || sh.dual) ? 1 : 0;
-        if (!(ok = take_k(seg.j0))) break;
-        for (int j = seg.j0; ok && j < seg.j1; ++j) {
-          if (ahead && j + 1 < seg.j1 && !(ok = take_k(j + 1))) break;
-          if (!(ok = take_v(j))) break;
-          if (!ahead && j + 1 < seg.j1 && !(ok = take_k(j + 1))) break;
+        // S(j + 1) goes before PV(j) where its region is free of P(j): P has a region
+        // of its own (d = 64), or the next block is the other side's (dual).
+        // Otherwise S(j + 1) overwrites P(j) and follows PV(j).
+        if (sh.dual) {
+          const std::true_type alt{};
+          const bool works = t == 0;
+          ok = take_k(seg.j0, alt, works);
+          for (int j = seg.j0; ok && j < seg.j1; ++j) {
+            if (j + 1 < seg.j1) ok = take_k(j + 1, alt, works);
+            ok = ok && take_v(j, alt, works);
+          }
+        } else {
+          const std::false_type own{};
+          ok = take_k(seg.j0, own, seg.j0 < end);
+          for (int j = seg.j0; ok && j < seg.j1; ++j) {
+            const bool works = j < end, next = j + 1 < seg.j1;
+            if (C::SEP_P && next) ok = take_k(j + 1, own, j + 1 < end);
+            ok = ok && take_v(j, own, works);
+            if (!C::SEP_P && next) ok = ok && take_k(j + 1, own, j + 1 < end);
+          }
         }
         if (!ok) break;
         if (fresh) mma_commit(&bar.o_full[t]);
