@@ -2,7 +2,7 @@
 
 Argument marshalling only: each ``sigattn_*`` function here passes device
 pointers, sizes and the current CUDA stream to the function of the same name
-in ``libsigattn.so``; every step of the computation runs in the library's CUDA
+in ``libsigattn.so`` (the paged calls through ``_binding.so``); every step of the computation runs in the library's CUDA
 kernels. PyTorch provides device memory and streams. There is no fallback: if
 the library is missing or a call fails, an exception is raised.
 
@@ -323,89 +323,47 @@ def sigattn_bwd_dkdv_varlen(q, k, v, dout, dk, dv, cu_seqlens, max_seqlen: int, 
 # ---------------------------------------------------------------------------
 # Serving from a paged cache (see the C header for the conventions)
 # ---------------------------------------------------------------------------
-# These checks run before every single-token call, whose kernels take a few
-# microseconds: each is one cheap comparison, and says what is wrong elsewhere.
-_i32, _bf16, _u8 = torch.int32, torch.bfloat16, torch.uint8
+# Checked and marshalled in C++ (csrc/binding.cpp), in the order of these
+# parameters: the kernels of a serving step take a few microseconds each, and
+# checks here with ctypes below them took longer.
+_calls = None
 
 
-def _refuse(t, name: str, dtype, dev: int, count=None):
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, expected the current device cuda:{dev}")
-    if t.dtype is not dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
-    raise ValueError(f"{name} has {t.numel()} elements, expected {count}")
+def _paged():
+    global _calls
+    if _calls is None:
+        library()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise RuntimeError("_binding.so is missing: run `python -m sigmoid_attention_b200.build` first") from e
+        _calls = module
+    return _calls
 
 
-def _arg(t, name: str, dtype, dev: int) -> int:
-    """Pointer of a contiguous tensor on the device `dev`, which is the current
-    one (the library launches on it)."""
-    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
-        _refuse(t, name, dtype, dev)
-    return t.data_ptr()
-
-
-def _ints(t, name: str, count: int, dev: int) -> int:
-    """The same for `count` int32 values."""
-    if t.get_device() != dev or t.dtype is not _i32 or t.numel() != count or not t.is_contiguous():
-        _refuse(t, name, _i32, dev, count)
-    return t.data_ptr()
-
-
-def _rows(t, name: str, rows: int, heads: int, d: int, dev: int):
-    """Pointer and row stride of [rows, heads, d] bf16 values whose rows may be
-    strided (slices of one fused projection)."""
-    if t.get_device() != dev:
-        _refuse(t, name, _bf16, dev)
-    if t.dtype is not _bf16 or tuple(t.shape) != (rows, heads, d):
-        raise ValueError(f"{name} must be a [{rows}, {heads}, {d}] CUDA torch.bfloat16 tensor, got {tuple(t.shape)} {t.dtype}")
-    s, sh, sd = t.stride()
-    if (sd != 1 and d > 1) or (sh != d and heads > 1):
-        raise ValueError(f"{name} must be contiguous within each row")
-    return t.data_ptr(), s if rows > 1 else heads * d
-
-
-def _cache(k_cache, v_cache, dev: int):
-    shape = k_cache.shape
-    if len(shape) != 4 or v_cache.shape != shape:
-        raise ValueError("k_cache and v_cache must be [num_pages, Hkv, page_size, d] tensors of one shape")
-    return _arg(k_cache, "k_cache", _bf16, dev), _arg(v_cache, "v_cache", _bf16, dev), *shape
-
-
-def _table(t, B: int, dev: int):
-    if t.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    width = t.shape[1]
-    return _ints(t, "block_table", B * width, dev), width
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def sigattn_paged_reserve(cached_lens, new_lens, block_table, free_pages, free_count, free_count_out, cu_seqlens,
                           kv_lens, slots, positions, page_size: int, workspace, stream=None) -> None:
     """Take pages for new_lens[b] more tokens of every sequence and write
     cu_seqlens, kv_lens, slots and positions (None to omit) for them."""
-    dev = torch.cuda.current_device()
-    B, rows = cached_lens.numel(), slots.numel()
-    table, width = _table(block_table, B, dev)
-    _check("sigattn_paged_reserve", library().sigattn_paged_reserve(
-        _ints(cached_lens, "cached_lens", B, dev), _ints(new_lens, "new_lens", B, dev), table,
-        _arg(free_pages, "free_pages", _i32, dev), _ints(free_count, "free_count", 1, dev),
-        _ints(free_count_out, "free_count_out", 1, dev), _ints(cu_seqlens, "cu_seqlens", B + 1, dev),
-        _ints(kv_lens, "kv_lens", B, dev), _arg(slots, "slots", _i32, dev),
-        None if positions is None else _ints(positions, "positions", rows, dev), B, width, page_size,
-        free_pages.numel(), rows, _arg(workspace, "workspace", _u8, dev), workspace.numel(), _stream_ptr(stream)))
+    st = (_calls or _paged()).paged_reserve(
+        cached_lens, new_lens, block_table, free_pages, free_count, free_count_out, cu_seqlens, kv_lens, slots, positions,
+        page_size, workspace, _handle(stream))
+    if st:
+        _check("sigattn_paged_reserve", st)
 
 
 def sigattn_paged_release(kv_lens, keep_lens, block_table, free_pages, free_count, free_count_out, page_size: int,
                           workspace, stream=None) -> None:
     """Push the pages past each sequence's first keep_lens[b] tokens (None: all
     pages) back on the stack of free pages."""
-    dev = torch.cuda.current_device()
-    B = kv_lens.numel()
-    table, width = _table(block_table, B, dev)
-    _check("sigattn_paged_release", library().sigattn_paged_release(
-        _ints(kv_lens, "kv_lens", B, dev), None if keep_lens is None else _ints(keep_lens, "keep_lens", B, dev), table,
-        _arg(free_pages, "free_pages", _i32, dev), _ints(free_count, "free_count", 1, dev),
-        _ints(free_count_out, "free_count_out", 1, dev), B, width, page_size, free_pages.numel(),
-        _arg(workspace, "workspace", _u8, dev), workspace.numel(), _stream_ptr(stream)))
+    st = (_calls or _paged()).paged_release(
+        kv_lens, keep_lens, block_table, free_pages, free_count, free_count_out, page_size, workspace, _handle(stream))
+    if st:
+        _check("sigattn_paged_release", st)
 
 
 def sigattn_paged_write(k, v, slots, k_cache, v_cache, workspace, q=None, q_out=None, positions=None, inv_freq=None,
@@ -413,35 +371,11 @@ def sigattn_paged_write(k, v, slots, k_cache, v_cache, workspace, q=None, q_out=
     """Store the rows of k and v ([rows, Hkv, d]) in their slots. With inv_freq
     (fp32 [pairs]) the keys, and q into q_out, are turned by positions
     (int32 [rows] or [axes, rows]; pair_axis int32 [pairs] names each pair's
-    axis)."""
-    dev = torch.cuda.current_device()
-    kc, vc, pages, Hkv, ps, d = _cache(k_cache, v_cache, dev)
-    rows = k.shape[0]
-    kp, ks = _rows(k, "k", rows, Hkv, d, dev)
-    vp, vs = _rows(v, "v", rows, Hkv, d, dev)
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
-    qp = qo = pp = fp = ap = None
-    Hq = qs = qos = pairs = 0
-    axes = 1
-    if q is not None:
-        Hq = q.shape[1]
-        qp, qs = _rows(q, "q", rows, Hq, d, dev)
-        qo, qos = _rows(q_out, "q_out", rows, Hq, d, dev)
-    if inv_freq is not None:
-        if positions is None:
-            raise ValueError("inv_freq needs positions")
-        pairs = inv_freq.numel()
-        fp = _arg(inv_freq, "inv_freq", torch.float32, dev)
-        if positions.dim() > 1:
-            axes = positions.shape[0]
-        pp = _ints(positions, "positions", axes * rows, dev)
-        if pair_axis is not None:
-            ap = _ints(pair_axis, "pair_axis", pairs, dev)
-    _check("sigattn_paged_write", library().sigattn_paged_write(
-        kp, ks, vp, vs, _ints(slots, "slots", rows, dev), kc, vc, qp, qs, qo, qos, pp, fp, ap, axes, pairs,
-        1 if adjacent else 0, rows, Hq, Hkv, d, ps, pages, _arg(workspace, "workspace", _u8, dev), workspace.numel(),
-        _stream_ptr(stream)))
+    axis). Rows of k, v, q and q_out may be strided."""
+    st = (_calls or _paged()).paged_write(
+        k, v, slots, k_cache, v_cache, workspace, q, q_out, positions, inv_freq, pair_axis, adjacent, _handle(stream))
+    if st:
+        _check("sigattn_paged_write", st)
 
 
 def sigattn_paged_workspace_size(Hq: int, Hkv: int, d: int, max_seqlen_q: int) -> int:
@@ -452,20 +386,10 @@ def sigattn_fwd_paged(q, k_cache, v_cache, o, cu_seqlens, kv_lens, block_table, 
                       workspace, stream=None) -> None:
     """Attention of the new tokens' q ([total, Hq, d], rows may be strided) over
     the cached keys and values; o is [total, Hq, d]."""
-    dev = torch.cuda.current_device()
-    kc, vc, pages, Hkv, ps, d = _cache(k_cache, v_cache, dev)
-    if q.dim() != 3:
-        raise ValueError("q must be [total, Hq, d]")
-    total, Hq, _ = q.shape
-    qp, qs = _rows(q, "q", total, Hq, d, dev)
-    if o.shape != q.shape:
-        raise ValueError("o must have q's shape")
-    B = kv_lens.numel()
-    table, width = _table(block_table, B, dev)
-    _check("sigattn_fwd_paged", library().sigattn_fwd_paged(
-        qp, qs, kc, vc, _arg(o, "o", _bf16, dev), _ints(cu_seqlens, "cu_seqlens", B + 1, dev),
-        _ints(kv_lens, "kv_lens", B, dev), table, B, Hq, Hkv, max_seqlen_q, total, width, ps, pages, d,
-        1 if causal else 0, _arg(workspace, "workspace", _u8, dev), workspace.numel(), _stream_ptr(stream)))
+    st = (_calls or _paged()).fwd_paged(
+        q, k_cache, v_cache, o, cu_seqlens, kv_lens, block_table, max_seqlen_q, causal, workspace, _handle(stream))
+    if st:
+        _check("sigattn_fwd_paged", st)
 
 
 def sigattn_plan(lengths, B, H, Lmax, d, kind, workspace, stream=None) -> None:

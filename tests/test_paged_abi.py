@@ -113,12 +113,17 @@ def test_attend_refusals(mem, change, status):
         a["ws_bytes"], None) == status
 
 
-def test_binding_rejects_cpu_tensors():
+def test_binding_rejects_cpu_tensors_and_other_objects():
     z = torch.zeros(2, 1, 64, dtype=torch.bfloat16)
     cache = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16)
-    i = torch.zeros(2, dtype=torch.int32)
-    with pytest.raises((ValueError, RuntimeError, AssertionError)):
-        sa.sigattn_fwd_paged(z, cache, cache, z, torch.zeros(3, dtype=torch.int32), i, i.view(2, 1), 1, True,
-                             torch.zeros(256, dtype=torch.uint8))
-    with pytest.raises((ValueError, RuntimeError, AssertionError)):
-        sa.sigattn_paged_write(z, z, i, cache, cache, torch.zeros(256, dtype=torch.uint8))
+    i, ws = torch.zeros(2, dtype=torch.int32), torch.zeros(256, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="k_cache"):
+        sa.sigattn_fwd_paged(z, cache, cache, z, torch.zeros(3, dtype=torch.int32), i, i.view(2, 1), 1, True, ws)
+    with pytest.raises(ValueError, match="k_cache"):
+        sa.sigattn_paged_write(z, z, i, cache, cache, ws)
+    with pytest.raises(ValueError, match="cached_lens"):
+        sa.sigattn_paged_reserve(i, i, i.view(2, 1), i, i[:1], i[:1], i, i, i, None, 16, ws)
+    with pytest.raises(ValueError, match="kv_lens"):
+        sa.sigattn_paged_release(i, None, i.view(2, 1), i, i[:1], i[:1], 16, ws)
+    with pytest.raises(ValueError, match="must be a tensor"):
+        sa.sigattn_paged_release([1, 2], None, i.view(2, 1), i, i[:1], i[:1], 16, ws)

@@ -466,6 +466,37 @@ def test_attend_bad_pages_contribute_nothing(q, causal):
     b.check(o, causal, skip={1: range(48, 64), 2: range(16), 0: range(80, 90)})
 
 
+def test_binding_refusals():
+    """Tensors of another type, shape, layout or size than a call takes."""
+    b = Batch([1, 1], [20, 40], 4, 2, 64, 16)
+    o, good = torch.empty_like(b.q), dict(q=b.q, k_cache=b.k_cache, v_cache=b.v_cache, cu=b.cu, kv=b.kv, table=b.table, ws=b.ws)
+
+    def call(o=o, **change):
+        a = {**good, **change}
+        sa.sigattn_fwd_paged(a["q"], a["k_cache"], a["v_cache"], o, a["cu"], a["kv"], a["table"], 1, True, a["ws"])
+
+    call()
+    for bad in (dict(q=b.q.float()), dict(q=b.q.cpu()), dict(q=b.q[:, :, :32]), dict(q=b.q.transpose(0, 1)),
+                dict(k_cache=b.k_cache.half()), dict(v_cache=b.v_cache[:1]), dict(k_cache=b.k_cache.transpose(2, 3)),
+                dict(cu=b.cu[:2]), dict(cu=b.cu.long()), dict(kv=b.kv.float()), dict(table=b.table[:1]),
+                dict(table=b.table.reshape(-1)), dict(table=b.table.t()), dict(ws=b.ws.float()), dict(o=o[:1]),
+                dict(o=o.float()), dict(o=None), dict(q=7)):
+        with pytest.raises(ValueError):
+            call(**bad)
+    with pytest.raises(sa.SigattnError):
+        call(ws=b.ws[:256])  # too small
+    with pytest.raises((TypeError, ValueError)):
+        sa.sigattn_fwd_paged(b.q, b.k_cache, b.v_cache, o, b.cu, b.kv, b.table, "one", True, b.ws)
+    k = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device=DEV)
+    for bad in (dict(k=k[:1]), dict(slots=i32([1])), dict(q=k, q_out=None), dict(inv_freq=torch.ones(8, device=DEV)),
+                dict(inv_freq=torch.ones(8, device=DEV), positions=i32([1])),
+                dict(inv_freq=torch.ones(8, device=DEV), positions=i32([1, 2]), pair_axis=i32([0]))):
+        a = {**dict(k=k, v=k, slots=i32([0, 1])), **bad}
+        with pytest.raises(ValueError):
+            sa.sigattn_paged_write(a.pop("k"), a.pop("v"), a.pop("slots"), b.k_cache, b.v_cache, b.ws, **a)
+    b.fine()
+
+
 @pytest.mark.parametrize("long", [False, True])
 def test_attend_bad_sequences_get_no_work(long):
     m = 100 if long else 1
