@@ -275,7 +275,8 @@ SIGATTN_API int sigattn_bwd_dkdv_varlen(const void* q, const void* k, const void
  *  - positions [rows] (optional, NULL to omit): each new token's position in
  *    its sequence, cached + 0, 1, ...; rows past the last get 0;
  *  - *free_count_out: the pages left (may be the same word as free_count).
- * num_pages is the capacity of free_pages and the bound on page numbers.
+ * num_pages is the capacity of free_pages and the bound on page numbers;
+ * rows <= 2^30.
  * The request is met whole or not at all. If a length is negative, a
  * sequence would exceed max_pages * page_size tokens, the new tokens exceed
  * `rows`, or the stack holds too few pages, then the error word is raised
@@ -309,7 +310,8 @@ SIGATTN_API int sigattn_paged_release(const int32_t* kv_lens, const int32_t* kee
  * slot slots[t] of k_cache and v_cache; slot -1 stores nothing (another slot
  * outside the cache stores nothing and raises site 204). Slots other than -1
  * must be distinct: which row a repeated slot ends up with is not defined.
- *  - q, q_out (both or neither; `rows` rows of [Hq][d], any Hq >= 1): q_out
+ *  - q, q_out (both or neither; `rows` rows of [Hq][d], Hq >= 1, Hq + 2 Hkv <=
+ *    4096): q_out
  *    receives the turned queries of every row, whatever its slot; q_out may
  *    be q itself (same stride).
  *  - Rotary positions: `pairs` > 0 pairs of values of each head are turned

@@ -184,6 +184,7 @@ void sigattn::set_last_error(const char* msg) { snprintf(g_last_error, sizeof(g_
 namespace {
 
 constexpr size_t kHeaderBytes = static_cast<size_t>(kHeaderWords) * 4;
+constexpr int kMaxReserveRows = 1 << 30;
 constexpr int kMaxWriteHeads = 4096;  // Hq + 2 Hkv of a cache write
 
 bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -591,6 +592,7 @@ int sigattn_paged_reserve(const int32_t* cached_lens, const int32_t* new_lens, i
     if (!aligned4(p)) return SIGATTN_ERR_INVALID_ARG;
   if (rows < 0 || (rows > 0 && !aligned4(slots)) || (positions != nullptr && !aligned4(positions)))
     return SIGATTN_ERR_INVALID_ARG;
+  if (rows > kMaxReserveRows) return SIGATTN_ERR_UNSUPPORTED;
   st = check_paged_call(workspace, workspace_bytes, kHeaderBytes, &info);
   if (st != SIGATTN_OK) return st;
   const PagedReserve a{cached_lens, new_lens, block_table, free_pages, free_count, free_count_out, cu_seqlens, kv_lens,

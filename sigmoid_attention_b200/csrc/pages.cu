@@ -1,13 +1,15 @@
 // pages.cu -- the paged cache's bookkeeping: taking pages for new tokens
-// (sigattn_paged_reserve) and giving pages back (sigattn_paged_release).
+// (sigattn_paged_reserve) and giving pages back (sigattn_paged_release); and its
+// writer (sigattn_paged_write).
 //
-// Both turn per-sequence lengths into per-token and per-page work with prefix
-// sums over the batch (B <= 4096). Every CTA forms the whole sums itself from
-// the lengths (16 bytes per sequence, from L2), so one launch does the call and
+// The bookkeeping turns per-sequence lengths into per-token and per-page work with
+// prefix sums over the batch (B <= 4096). Every CTA forms the whole sums itself
+// from the lengths (8 bytes per sequence, from L2), so one launch does the call and
 // no CTA waits for another; the CTAs then share the tokens and pages out. Words
 // that a caller may pass as input and output at once (the stack height, the
-// lengths) are written by the CTA that finishes last, when every CTA has read
-// them.
+// lengths) are written by the CTA that came last to have read them.
+// Latency bounds both calls (a few thousand bytes): what counts is the chain
+// lengths -> sums -> pages -> slots, one trip to memory each.
 #include "paged.cuh"
 
 namespace sigattn {
@@ -16,40 +18,33 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Exclusive prefix sums over the CTA of one pair of 64-bit values per thread
-// (64 bits: a batch of bad lengths may add up to more than 32); the totals
-// go to *total_x, *total_y of every thread.
-__device__ __forceinline__ void block_scan2(long long& x, long long& y, long long* total_x, long long* total_y) {
-  __shared__ long long sums[2][kThreads / 32];
+// Exclusive prefix sums over the CTA of a pair of values per thread; the totals go
+// to *total_x, *total_y of every thread.
+__device__ __forceinline__ void block_scan2(uint32_t& x, uint32_t& y, uint32_t* total_x, uint32_t* total_y) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ uint2 sums[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long ix = x, iy = y;
+  auto scan = [&](uint2 v) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long ux = __shfl_up_sync(0xffffffffu, ix, o), uy = __shfl_up_sync(0xffffffffu, iy, o);
-    if (lane >= o) {
-      ix += ux;
-      iy += uy;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t ux = __shfl_up_sync(0xffffffffu, v.x, o), uy = __shfl_up_sync(0xffffffffu, v.y, o);
+      if (lane >= o) {
+        v.x += ux;
+        v.y += uy;
+      }
     }
-  }
-  if (lane == 31) {
-    sums[0][warp] = ix;
-    sums[1][warp] = iy;
-  }
+    return v;
+  };
+  const uint2 incl = scan(make_uint2(x, y));
+  if (lane == 31) sums[warp] = incl;
   __syncthreads();
-  long long bx = 0, by = 0, tx = 0, ty = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w == warp) {
-      bx = tx;
-      by = ty;
-    }
-    tx += sums[0][w];
-    ty += sums[1][w];
-  }
-  x = bx + ix - x;
-  y = by + iy - y;
-  *total_x = tx;
-  *total_y = ty;
+  const uint2 upto = scan(lane < kWarps ? sums[lane] : make_uint2(0, 0));
+  *total_x = __shfl_sync(0xffffffffu, upto.x, kWarps - 1);
+  *total_y = __shfl_sync(0xffffffffu, upto.y, kWarps - 1);
+  const uint32_t bx = __shfl_sync(0xffffffffu, upto.x, warp > 0 ? warp - 1 : 0);
+  const uint32_t by = __shfl_sync(0xffffffffu, upto.y, warp > 0 ? warp - 1 : 0);
+  x = (warp > 0 ? bx : 0) + incl.x - x;
+  y = (warp > 0 ? by : 0) + incl.y - y;
 }
 
 // The last b with off[b] <= i, for off[0] = 0 <= i < off[B] (so sequence b
@@ -63,20 +58,16 @@ __device__ __forceinline__ int owner(const int* off, int B, int i) {
   return lo;
 }
 
-// Whether this CTA is the last of the grid to come here (uniform over the
-// CTA); the header's ticket word is back at zero afterwards. What every other
-// CTA read or wrote before is ordered before what the last one does next.
-__device__ __forceinline__ bool last_cta(int* ws) {
-  __shared__ int last;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    last = gridDim.x == 1 || atomicAdd(ws + kHdrTicket, 1) == static_cast<int>(gridDim.x) - 1;
-    if (last) ws[kHdrTicket] = 0;
-    __threadfence();
-  }
-  __syncthreads();
-  return last != 0;
+// Pages of n tokens.
+__device__ __forceinline__ int pages_of(int n, int shift) { return (n + (1 << shift) - 1) >> shift; }
+
+// Thread 0 of a CTA that has read all it needs of the lengths and the height:
+// whether it is the grid's last (the ticket word is then back at zero).
+__device__ __forceinline__ bool last_reader(int* ws) {
+  if (gridDim.x == 1) return true;
+  if (atomicAdd(ws + kHdrTicket, 1) != static_cast<int>(gridDim.x) - 1) return false;
+  ws[kHdrTicket] = 0;
+  return true;
 }
 
 }  // namespace
@@ -85,42 +76,54 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(PagedReserve a) {
   grid_dep_launch();
   grid_dep_wait();
   extern __shared__ int smem_pages[];
-  __shared__ int s_bad;
-  int* s_cu = smem_pages;                // [B + 1] new tokens before sequence b
-  int* s_pg = smem_pages + a.B + 1;      // [B + 1] new pages before sequence b
+  __shared__ int s_bad, s_last, s_count;
+  __shared__ float s_tokens;
+  int* s_cached = smem_pages;          // [B] tokens before the call
+  int* s_cu = s_cached + a.B;          // [B + 1] new tokens before sequence b
+  int* s_pg = s_cu + a.B + 1;          // [B + 1] new pages before sequence b
   const int tid = threadIdx.x;
   const int sh = a.page_shift, ps = 1 << sh;
   const int most = a.max_pages << sh;
-  if (tid == 0) s_bad = a.B;
-  __syncthreads();
+  if (tid == 0) {
+    s_bad = a.B;
+    s_tokens = 0.f;
+    s_count = *a.free_count;  // read by one thread, so that its CTA has read it where it says so
+  }
   const int per = ceil_div(a.B, kThreads);
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  const int count = *a.free_count;
-  long long tok = 0, pg = 0;
+  uint32_t tok = 0, pg = 0;
+  float tokens = 0.f;  // so many that 32 bits would not hold them show here
+  int worst = a.B;
   for (int b = b0; b < b1; ++b) {
     const int c = a.cached[b], m = a.fresh[b];
+    s_cached[b] = c;
+    s_cu[b] = m;
     if (c < 0 || m < 0 || c > most || m > most - c) {
-      atomicMin(&s_bad, b);
+      worst = min(worst, b);
     } else {
       tok += m;
-      pg += ((c + m + ps - 1) >> sh) - ((c + ps - 1) >> sh);
+      tokens += m;
+      pg += pages_of(c + m, sh) - pages_of(c, sh);
     }
   }
-  long long total_tok, total_pg;
-  block_scan2(tok, pg, &total_tok, &total_pg);  // its barrier also covers s_bad
-  const int bad = s_bad;
-  const bool few = count < 0 || count > a.num_pages || total_pg > count;
-  const bool ok = bad == a.B && total_tok <= a.rows && !few;
-  if (!ok && blockIdx.x == 0 && tid == 0)
-    raise_invalid(a.ws, bad < a.B ? -(bad + 1) : total_tok > a.rows ? 201 : 202);
-  if (ok) {
-    for (int b = b0; b < b1; ++b) {
-      const int c = a.cached[b], m = a.fresh[b];
-      s_cu[b] = static_cast<int>(tok);
-      s_pg[b] = static_cast<int>(pg);
-      tok += m;
-      pg += ((c + m + ps - 1) >> sh) - ((c + ps - 1) >> sh);
-    }
+  __syncthreads();
+  if (worst < a.B) atomicMin(&s_bad, worst);
+  if (tokens > 1e6f) atomicAdd(&s_tokens, tokens);
+  uint32_t total_tok, total_pg;
+  block_scan2(tok, pg, &total_tok, &total_pg);  // its barrier also covers s_bad and s_tokens
+  // Every thread of the CTA has its lengths and the height.
+  if (tid == 0) s_last = last_reader(a.ws);
+  const int bad = s_bad, count = s_count;
+  const bool many = s_tokens > 2e9f || total_tok > static_cast<uint32_t>(a.rows);
+  const bool few = count < 0 || count > a.num_pages || total_pg > static_cast<uint32_t>(count);
+  const bool ok = bad == a.B && !many && !few;
+  if (!ok && blockIdx.x == 0 && tid == 0) raise_invalid(a.ws, bad < a.B ? -(bad + 1) : many ? 201 : 202);
+  for (int b = b0; b < b1; ++b) {
+    const int c = s_cached[b], m = ok ? s_cu[b] : 0;
+    s_cu[b] = ok ? static_cast<int>(tok) : 0;
+    s_pg[b] = ok ? static_cast<int>(pg) : 0;
+    tok += m;
+    pg += pages_of(c + m, sh) - pages_of(c, sh);
   }
   const int T = ok ? static_cast<int>(total_tok) : 0, P = ok ? static_cast<int>(total_pg) : 0;
   if (tid == 0) {
@@ -128,50 +131,48 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(PagedReserve a) {
     s_pg[a.B] = P;
   }
   __syncthreads();
-  const int gid = blockIdx.x * kThreads + tid, gsize = gridDim.x * kThreads;
-
-  // New table entries: new page i (in batch order) is stack[count - 1 - i].
-  for (int i = gid; i < P; i += gsize) {
-    const int b = owner(s_pg, a.B, i);
-    const int k = ((a.cached[b] + ps - 1) >> sh) + i - s_pg[b];
-    int page = a.free_pages[count - 1 - i];
-    if (page < 0 || page >= a.num_pages) {
-      raise_invalid(a.ws, 203);
-      page = -1;
+  if (s_last) {
+    for (int b = tid; b <= a.B; b += kThreads) {
+      a.cu[b] = s_cu[b];
+      if (b < a.B) a.kv[b] = s_cached[b] + s_cu[b + 1] - s_cu[b];
     }
-    a.table[static_cast<size_t>(b) * a.max_pages + k] = page;
+    if (tid == 0) *a.free_count_out = count - P;
   }
+
   // Slots and positions, four consecutive rows per thread and step: one search
-  // for the first, the others by counting on. Pages of new tokens past the
-  // ones in use come from the stack, so no CTA reads what another one wrote.
+  // for the first, the others by counting on. New page i (in batch order) is
+  // stack[count - 1 - i]; it starts with a new token, whose thread enters it in
+  // the table. Pages past the ones in use come from the stack, so no CTA reads
+  // what another one wrote.
   const bool wide = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15u) == 0;
   const int groups = a.rows / 4 + (a.rows % 4 != 0);
-  for (int g = gid; g < groups; g += gsize) {
+  for (int g = blockIdx.x * kThreads + tid; g < groups; g += gridDim.x * kThreads) {
     const int t0 = 4 * g;
     int slot[4] = {-1, -1, -1, -1}, at[4] = {0, 0, 0, 0};
     if (t0 < T) {
       int b = owner(s_cu, a.B, t0);
-      int c = a.cached[b], have = (c + ps - 1) >> sh, seen = -1, page = -1;
+      int c = s_cached[b], have = pages_of(c, sh), seen = -1, page = -1;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int t = t0 + e;
         if (t >= T) break;
         if (t >= s_cu[b + 1]) {
           do ++b; while (t >= s_cu[b + 1]);
-          c = a.cached[b];
-          have = (c + ps - 1) >> sh;
+          c = s_cached[b];
+          have = pages_of(c, sh);
           seen = -1;
         }
         at[e] = c + t - s_cu[b];
         const int k = at[e] >> sh;
         if (k != seen) {
           seen = k;
-          page = k < have ? a.table[static_cast<size_t>(b) * a.max_pages + k]
-                          : a.free_pages[count - 1 - (s_pg[b] + k - have)];
+          int* entry = a.table + static_cast<size_t>(b) * a.max_pages + k;
+          page = k < have ? *entry : a.free_pages[count - 1 - (s_pg[b] + k - have)];
           if (page < 0 || page >= a.num_pages) {
             raise_invalid(a.ws, 203);
             page = -1;
           }
+          if (k >= have && (at[e] & (ps - 1)) == 0) *entry = page;
         }
         if (page >= 0) slot[e] = (page << sh) + (at[e] & (ps - 1));
       }
@@ -186,75 +187,102 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(PagedReserve a) {
       }
     }
   }
-
-  if (!last_cta(a.ws)) return;
-  for (int b = tid; b <= a.B; b += kThreads) {
-    a.cu[b] = ok ? s_cu[b] : 0;
-    if (b < a.B) a.kv[b] = a.cached[b] + (ok ? s_cu[b + 1] - s_cu[b] : 0);
-  }
-  if (tid == 0) *a.free_count_out = count - P;
 }
 
 __global__ void __launch_bounds__(kThreads) release_kernel(PagedRelease a) {
   grid_dep_launch();
   grid_dep_wait();
   extern __shared__ int smem_pages[];
-  __shared__ int s_bad;
-  int* s_pg = smem_pages;  // [B + 1] released pages before sequence b
+  __shared__ int s_bad, s_count;
+  __shared__ float s_pages;
+  int* s_pg = smem_pages;           // [B + 1] released pages before sequence b
+  int* s_first = s_pg + a.B + 1;    // [B] the first page it gives back
   const int tid = threadIdx.x;
-  const int sh = a.page_shift, ps = 1 << sh;
+  const int sh = a.page_shift;
   const int most = a.max_pages << sh;
-  if (tid == 0) s_bad = a.B;
-  __syncthreads();
+  if (tid == 0) {
+    s_bad = a.B;
+    s_pages = 0.f;
+    s_count = *a.free_count;
+  }
   const int per = ceil_div(a.B, kThreads);
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  const int count = *a.free_count;
-  long long pg = 0, unused = 0;
+  uint32_t pg = 0, unused = 0, total, total_unused;
+  float pages = 0.f;
+  int worst = a.B;
   for (int b = b0; b < b1; ++b) {
     const int n = a.kv[b], keep = a.keep ? a.keep[b] : 0;
-    if (keep < 0 || n < keep || n > most) atomicMin(&s_bad, b);
-    else pg += ((n + ps - 1) >> sh) - ((keep + ps - 1) >> sh);
+    const bool bad = keep < 0 || n < keep || n > most;
+    const int gone = bad ? 0 : pages_of(n, sh) - pages_of(keep, sh);
+    if (bad) worst = min(worst, b);
+    s_first[b] = bad ? 0 : pages_of(keep, sh);
+    s_pg[b] = gone;
+    pg += gone;
+    pages += gone;
   }
-  long long total, total_unused;
+  __syncthreads();
+  if (worst < a.B) atomicMin(&s_bad, worst);
+  if (pages > 1e6f) atomicAdd(&s_pages, pages);
   block_scan2(pg, unused, &total, &total_unused);
-  const int bad = s_bad;
-  const bool ok = bad == a.B && count >= 0 && total <= a.num_pages - count;
-  if (!ok && blockIdx.x == 0 && tid == 0) raise_invalid(a.ws, bad < a.B ? -(bad + 1) : 202);
-  if (ok) {
-    for (int b = b0; b < b1; ++b) {
-      const int n = a.kv[b], keep = a.keep ? a.keep[b] : 0;
-      s_pg[b] = static_cast<int>(pg);
-      pg += ((n + ps - 1) >> sh) - ((keep + ps - 1) >> sh);
-    }
-  }
+  const int bad = s_bad, count = s_count;
+  const bool fits = count >= 0 && count <= a.num_pages && s_pages < 2e9f &&
+                    total <= static_cast<uint32_t>(a.num_pages - count);
+  const bool ok = bad == a.B && fits;
   const int P = ok ? static_cast<int>(total) : 0;
-  if (tid == 0) s_pg[a.B] = P;
+  if (tid == 0) {
+    if (!ok && blockIdx.x == 0) raise_invalid(a.ws, bad < a.B ? -(bad + 1) : 202);
+    if (last_reader(a.ws)) *a.free_count_out = count + P;
+    s_pg[a.B] = P;
+  }
+  for (int b = b0; b < b1; ++b) {
+    const int gone = s_pg[b];
+    s_pg[b] = static_cast<int>(pg);
+    pg += gone;
+  }
   __syncthreads();
   for (int i = blockIdx.x * kThreads + tid; i < P; i += gridDim.x * kThreads) {
     const int b = owner(s_pg, a.B, i);
-    const int keep = a.keep ? a.keep[b] : 0;
-    int page = a.table[static_cast<size_t>(b) * a.max_pages + ((keep + ps - 1) >> sh) + i - s_pg[b]];
+    int page = a.table[static_cast<size_t>(b) * a.max_pages + s_first[b] + i - s_pg[b]];
     if (page < 0 || page >= a.num_pages) {
       raise_invalid(a.ws, 203);
       page = -1;
     }
     a.free_pages[count + i] = page;
   }
-  if (last_cta(a.ws) && tid == 0) *a.free_count_out = count + P;
 }
 
+namespace {
+
+// The lengths and sums of the largest batches take more than 48 KB.
+constexpr int kPagesSmem = (3 * kMaxBatch + 2) * static_cast<int>(sizeof(int));
+
+cudaError_t pages_setup() {
+  static PerDeviceOnce attr;
+  return attr.run([] {
+    const cudaError_t e = cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPagesSmem);
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(release_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPagesSmem);
+  });
+}
+
+}  // namespace
+
 cudaError_t launch_paged_reserve(const PagedReserve& a, int num_sms, cudaStream_t stream) {
-  const int smem = 2 * (a.B + 1) * static_cast<int>(sizeof(int));
+  const cudaError_t e = pages_setup();
+  if (e != cudaSuccess) return e;
+  const int smem = (3 * a.B + 2) * static_cast<int>(sizeof(int));
   const long long work = static_cast<long long>(a.rows) / 4 + 1;
   const int grid = static_cast<int>(std::max<long long>(1, std::min<long long>(2 * num_sms, (work + kThreads - 1) / kThreads)));
   return launch_programmatic(reserve_kernel, dim3(grid), dim3(kThreads), smem, stream, a);
 }
 
 cudaError_t launch_paged_release(const PagedRelease& a, int num_sms, cudaStream_t stream) {
-  const int smem = (a.B + 1) * static_cast<int>(sizeof(int));
+  const cudaError_t e = pages_setup();
+  if (e != cudaSuccess) return e;
+  const int smem = (2 * a.B + 1) * static_cast<int>(sizeof(int));
   const long long work = static_cast<long long>(a.B) * a.max_pages;
   const int grid =
-      static_cast<int>(std::max<long long>(1, std::min<long long>(num_sms, (work + 4 * kThreads - 1) / (4 * kThreads))));
+      static_cast<int>(std::max<long long>(1, std::min<long long>(2 * num_sms, (work + 4 * kThreads - 1) / (4 * kThreads))));
   return launch_programmatic(release_kernel, dim3(grid), dim3(kThreads), smem, stream, a);
 }
 

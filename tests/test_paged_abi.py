@@ -37,6 +37,7 @@ RESERVE = dict(cached=1, new=1, table=1, stack=1, count=1, count_out=1, cu=1, kv
     (dict(B=0), INVALID), (dict(B=4097), UNSUPPORTED), (dict(max_pages=0), INVALID), (dict(page=0), UNSUPPORTED),
     (dict(page=48), UNSUPPORTED), (dict(page=8), UNSUPPORTED), (dict(page=512), UNSUPPORTED),
     (dict(num_pages=0), INVALID), (dict(rows=-1), INVALID), (dict(max_pages=(1 << 20) + 1), UNSUPPORTED),
+    (dict(rows=(1 << 30) + 1), UNSUPPORTED),
     (dict(num_pages=1 << 27), UNSUPPORTED), (dict(ws=0), INVALID), (dict(ws_bytes=255), INVALID),
 ])
 def test_reserve_refusals(mem, change, status):
