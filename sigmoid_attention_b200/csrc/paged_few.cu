@@ -155,15 +155,12 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     tma_prefetch_desc(&tm_k);
   }
   if (lane == 0 && warp == kLoadV) tma_prefetch_desc(&tm_v);
-  // Query rows that no load covers stay zero.
-  for (int i = threadIdx.x; i < 2 * C::Q_BYTES / 16; i += C::THREADS)
-    reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
-  fence_proxy_async_smem();
   const int G = a.Hq / a.Hkv;
   grid_dep_launch();
   grid_dep_wait();
-  plan_run<C::THREADS>(a, &bar.run, [](const SeqInfo& s) -> U { return seq_blocks(s.n); },
-                       [&](const SeqInfo& s) { return a.cut * static_cast<float>(s.m * G) * seq_blocks(s.n); });
+  auto units = [](const SeqInfo& s) -> U { return seq_blocks(s.n); };
+  auto joins = [&](const SeqInfo& s) { return a.cut * static_cast<float>(s.m * G) * seq_blocks(s.n); };
+  if (a.B > kWarpPlan) plan_run<C::THREADS>(a, &bar.run, units, joins);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -174,7 +171,8 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     // Both walk the run; the K warp hands its segments to the other roles.
     const bool is_k = warp == kLoadK;
     const OneTile tiles{};
-    RunWalker<U, OneTile> walk(a, tiles, bar.run, lane);
+    const PlanRun<U> run = a.B > kWarpPlan ? bar.run : plan_warp<U>(a, units, joins);
+    RunWalker<U, OneTile> walk(a, tiles, run, lane);
     const Segment& seg = walk.seg;
     TileRing<D> ring{is_k ? &tm_k : &tm_v, smem + (is_k ? 0 : C::KST * C::TILE_BYTES), bar.full + (is_k ? 0 : C::KST),
                      bar.empty + (is_k ? 0 : C::KST), is_k ? C::KST : C::VST, 1 << walk.box_shift(), 0, 0, 0};

@@ -255,11 +255,12 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
   const TileMath math{T, a.causal};
   grid_dep_launch();
   grid_dep_wait();
-  plan_run<C::THREADS>(a, &bar.run, [&](const SeqInfo& s) { return math.before<U>(s, math.items(s)); },
-                       [&](const SeqInfo& s) {
-                         const float tiles = math.two(s, 0) ? 2.0f : 1.0f;
-                         return a.cut * tiles * tiles * static_cast<float>(min(s.m, 2 * T) * G) * seq_blocks(s.n);
-                       });
+  auto units = [&](const SeqInfo& s) { return math.before<U>(s, math.items(s)); };
+  auto joins = [&](const SeqInfo& s) {
+    const float tiles = math.two(s, 0) ? 2.0f : 1.0f;
+    return a.cut * tiles * tiles * static_cast<float>(min(s.m, 2 * T) * G) * seq_blocks(s.n);
+  };
+  if (a.B > kWarpPlan) plan_run<C::THREADS>(a, &bar.run, units, joins);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -281,7 +282,9 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
     // ------------------------------------- producers: segments, Q and K; V
     // Both walk the run; the K warp hands its segments to the other roles.
     const bool is_k = warp == kLoadK;
-    RunWalker<U, TileMath> walk(a, math, bar.run, lane);
+    const PlanRun<U> run = a.B > kWarpPlan ? bar.run : plan_warp<U>(a, units, joins);
+    if (is_k && lane == 0) bar.run.per = run.per;  // (read by the epilogue once it has a segment)
+    RunWalker<U, TileMath> walk(a, math, run, lane);
     const Segment& seg = walk.seg;
     TileRing<D> ring{is_k ? &tm_k : &tm_v, is_k ? sK : sV, is_k ? bar.k_full : bar.v_full, is_k ? bar.k_empty : bar.v_empty,
                      is_k ? C::KST : C::VST, 1 << walk.box_shift(), 0, 0, 0};
