@@ -707,7 +707,7 @@ int sigattn_fwd_paged(const void* q, long long q_stride, const void* k_cache, co
   const bool wide = units >= 2147483648.0;
   const PagedAttend a{static_cast<const bf16*>(q), static_cast<const bf16*>(k_cache), static_cast<const bf16*>(v_cache),
                       static_cast<bf16*>(o), q_stride, cu_seqlens, kv_lens, block_table, B, Hq, Hkv, max_seqlen_q, total,
-                      max_pages, shift, num_pages, d, causal != 0, few ? 1 : 2, few ? kFewCut : kManyCut,
+                      max_pages, shift, num_pages, d, causal != 0, few ? 1 : 4, few ? kFewCut : kManyCut,
                       reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes),
                       static_cast<int*>(workspace)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
