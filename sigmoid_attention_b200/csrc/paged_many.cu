@@ -26,7 +26,7 @@
 //    that all of them add to one O in order.
 //
 // Roles (20 warps): 0-15 epilogue (warps 0-7 tile 0, 8-15 tile 1; per tile, four
-// warps for each half of a block's keys), 16 and 17 the producers of K (and Q) and
+// warps for every other 32 of a block's keys), 16 and 17 the producers of K (and Q) and
 // of V, 18 and 19 the issuers of tiles 0 and 1.
 // TMEM: S of tile t at columns [128t, 128t + 128), O at 256 + t D; P over S
 // (d = 128) or in a region of its own after O (d = 64).
@@ -224,8 +224,8 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
     } else if (warp < 5) {
       const int t = warp - 3;
       mbar_init(&bar.s_full[t], 1);
-      mbar_init(&bar.p_full[2 * t], 4);
-      mbar_init(&bar.p_full[2 * t + 1], 4);
+      mbar_init(&bar.p_full[2 * t], 8);
+      mbar_init(&bar.p_full[2 * t + 1], 8);
       mbar_init(&bar.o_full[t], 1);
       mbar_init(&bar.o_empty[t], 8);
       mbar_init(&bar.epi_done[t], 8);
@@ -336,7 +336,11 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
       const uint64_t d_v = smem_desc_sw128(smem_u32(sV), C::BOX_BYTES, 1024);  // MN-major view of V
       constexpr uint64_t kTile = C::TILE_BYTES >> 4;
       const uint32_t tm_o = tmem + C::TM_O + t * D;
-      constexpr int kPHalf = C::SEP_P ? 32 : 64;
+      // Column of the weights of the kk-th sixteen keys of a block's half h. Where P
+      // lies over S, each 32 keys' weights start where their scores did.
+      auto p_at = [](const int h, const int kk) -> uint32_t {
+        return C::SEP_P ? h * 32 + kk * 8 : h * 64 + (kk >> 1) * 32 + (kk & 1) * 8;
+      };
       uint32_t kst = 0, kph = 0, vst = 0, vph = 0, qst = 0, qph = 0, oph = 0, rst = 0, rph = 0, segs = 0;
       // Per side e (bit e): parity of the blocks so far, and whether there were any.
       // Both issuers keep both sides' bits, since dual segments swap the issuer.
@@ -426,10 +430,10 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
               if (steps == 8) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                  mma_ts(tm_o, tm_p + h * kPHalf + kk * 8, b0 + ((kk * 2048) >> 4), idesc_o, (h > 0 || kk > 0) ? 1u : fresh);
+                  mma_ts(tm_o, tm_p + p_at(h, kk), b0 + ((kk * 2048) >> 4), idesc_o, (h > 0 || kk > 0) ? 1u : fresh);
               } else {
                 for (int kk = 0; kk < min(4, steps - 4 * h); ++kk)
-                  mma_ts(tm_o, tm_p + h * kPHalf + kk * 8, b0 + ((kk * 2048) >> 4), idesc_o, (h > 0 || kk > 0) ? 1u : fresh);
+                  mma_ts(tm_o, tm_p + p_at(h, kk), b0 + ((kk * 2048) >> 4), idesc_o, (h > 0 || kk > 0) ? 1u : fresh);
               }
             }
             podd ^= 1u << e;
@@ -482,10 +486,10 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
   } else {
     // ------------------------------------------------------------- epilogue
     const int t = warp >> 3;                       // side of this warp
-    const int h = (warp >> 2) & 1;                 // its half (64 keys) of each block
+    const int h = (warp >> 2) & 1;                 // its 32 keys of each half of a block
     const int r = threadIdx.x & 127;               // row within the tile = TMEM lane
     const uint32_t quad = tmem + (static_cast<uint32_t>(r & 96) << 16);
-    const uint32_t tS = quad + C::TM_S + t * 128 + h * 64;
+    const uint32_t tS = quad + C::TM_S + t * 128 + h * 32;
     constexpr float scale_l2e = Scale<D>::value * kLog2e;
     uint32_t rst = 0, rph = 0;
     // Bits in one register (the passes leave few): parities of the waits for S, O,
@@ -515,7 +519,12 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
       // (what their rows of P hold reaches no other row).
       const bool idle = __all_sync(0xffffffffu, !row_ok);
       const int plain = min(end, clear / kKeyBlock);  // blocks that every row sees whole
-      // One pass over key block j. How often this code exists decides how short
+      // One pass over key block j: a chunk of 32 keys from each half of the block,
+      // so that the product with the first half's weights runs while the second
+      // half's are computed (8 prompts of 512 tokens 57.6 -> 56.7 us, 24 short chunks
+      // at d = 64 18.1 -> 16.9 us against a half of the keys per warp; computing S in
+      // halves as well, so that the next block's first starts after that product,
+      // loses: 59.4 us). How often this code exists decides how short
       // texts run, whose passes wait for instructions (the forward kernel's
       // instances for masked and unmasked blocks with both chunks unrolled: 4500
       // cycles for a chunk instead of 800). At d = 128 one copy serves both chunks
@@ -542,7 +551,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
 #pragma unroll (C::SEP_P ? 2 : 1)
           for (int c = 0; c < 2; ++c) {
             uint32_t s[32];
-            tmem_ld32(tS + 32 * c, s);
+            tmem_ld32(tS + 64 * c, s);
             if (C::SEP_P && c == 1) {
               tc_fence_before();
               __syncwarp();
@@ -551,7 +560,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
             if (MODE == kMasked || (MODE == kEither && j >= plain)) {
               // One bit per key: tests of a word's bits go to predicates several at a
               // time, where 32 comparisons with `seen` take one instruction each.
-              const int left = seen - (j * kKeyBlock + h * 64 + 32 * c);
+              const int left = seen - (j * kKeyBlock + 64 * c + 32 * h);
               const uint32_t keep = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
@@ -565,9 +574,12 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
               bits ^= kPv;
               tc_fence_after();
             }
-            tmem_st16((C::SEP_P ? quad + C::TM_P + t * 64 + h * 32 : tS) + 16 * c, pk);
+            tmem_st16(C::SEP_P ? quad + C::TM_P + t * 64 + c * 32 + h * 16 : tS + 64 * c, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.p_full[2 * t + c]);
           }
-          tmem_st_wait();
         } else if (C::SEP_P) {
           if (lane == 0) mbar_arrive(&bar.s_read[t]);
           if (bits & kPending) {
@@ -576,10 +588,11 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
           }
         }
         if (C::SEP_P) bits |= kPending;
-        tc_fence_before();
-        __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&bar.p_full[2 * t + h]);
+          if (idle) {
+            mbar_arrive(&bar.p_full[2 * t]);
+            mbar_arrive(&bar.p_full[2 * t + 1]);
+          }
           if (joint) mbar_arrive(&bar.epi_done[t]);  // hand the turn over
         }
         return true;
