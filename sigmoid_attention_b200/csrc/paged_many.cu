@@ -64,11 +64,18 @@ struct ManyBarriers {
   uint64_t s_read[2];    // SEP_P: the epilogue copied tile t's S out of TMEM
   uint64_t pv_done[2];   // SEP_P: tile t's PV products of a block completed (P region free)
   uint64_t fin[2][4];    // issuer t's products of a segment completed (by segment, modulo 4)
-  uint64_t stored, counted, drain[2];
+  // Cut tiles of this CTA: [0] the run's first, if it began in another CTA's run and
+  // ends in this one, [1] the run's last, if it goes on in the next CTA's.
+  uint64_t stored[2], counted[2];
+  uint64_t ask, answered;  // [1]: should its part be stored at all?
+  uint64_t drain[2];
+  Segment cut[2];
+  int join[2];  // does this CTA add up the parts?
+  int keep;     // [1]: the other parts were there, so this CTA's stayed in tensor memory
   SegRing ring;
   PlanRun<U> run;
   uint32_t tmem_base;
-  int abort, last;
+  int abort;
 };
 
 // sum_{k < n} floor((x k + y) / 128), x n and y less than 2^25. Where x is a power
@@ -235,8 +242,9 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
     } else if (warp == 5) {
       for (int s = 0; s < 4; ++s) { mbar_init(&bar.fin[0][s], 1); mbar_init(&bar.fin[1][s], 1); }
     } else {
-      mbar_init(&bar.stored, C::EPI_WARPS);
-      mbar_init(&bar.counted, 1);
+      for (int k = 0; k < 2; ++k) { mbar_init(&bar.stored[k], C::EPI_WARPS); mbar_init(&bar.counted[k], 1); }
+      mbar_init(&bar.ask, 1);
+      mbar_init(&bar.answered, 1);
       seg_ring_init(bar.ring, C::EPI_WARPS + 2);
     }
     fence_mbar_init();
@@ -270,6 +278,10 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
     const bool two = seg.tile * 2 * T + T < seg.m;
     return Shape{two, !two && seg.j1 - seg.j0 > 1};
   };
+  // Does the CTA of a tile's first part look whether the rest is there before it
+  // stores its own? (Not with more than two parts: all but the last come from
+  // CTAs that do nothing else, and end together.)
+  auto asks = [](const Segment& seg) { return seg.j0 == 0 && seg.last_cta == seg.first_cta + 1; };
   // Side t of a segment that is not dual works on blocks [j0, end): none where
   // its tile has no tokens or its rows see none of them.
   auto side_end = [&](const Segment& seg, int t) {
@@ -289,9 +301,30 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
     TileRing<D> ring{is_k ? &tm_k : &tm_v, is_k ? sK : sV, is_k ? bar.k_full : bar.v_full, is_k ? bar.k_empty : bar.v_empty,
                      is_k ? C::KST : C::VST, 1 << walk.box_shift(), 0, 0, 0};
     uint32_t rst = 0, rph = 0, qst = 0, qph = 0, q_loads = 0;
+    // Parts that this CTA has still to count (K warp; bits as in bar.cut). It counts
+    // the first tile's between two loads, once they are stored, so that they cost the
+    // epilogue its stores and no more (an epilogue that counts waits until the
+    // stores of all SMs have drained, 9000 cycles). The last tile's it handles after
+    // its last load: while the last products still run it looks whether the
+    // other parts are there already. They mostly are, and then the epilogue
+    // adds them to its own sum as it reads that from tensor memory, instead of
+    // storing and reading it (both: two sequences of 4096 tokens of 16 heads 173 -> 167
+    // us, eight of 512 tokens of 32 heads 56.8 -> 52.7 us).
+    int cut = 0;
+    auto count_part = [&](const int k) {
+      if (lane == 0) {
+        bar.join[k] = part_count(bar.cut[k], ws);
+        mbar_arrive(&bar.counted[k]);
+      }
+      __syncwarp();
+      cut &= ~(1 << k);
+    };
     bool ok = true;
     while (ok && walk.advance()) {
       if (is_k) {
+        const bool tail = seg.j1 < seg.blocks;
+        if (lane == 0 && (tail || seg.j0 > 0)) bar.cut[tail ? 1 : 0] = seg;
+        cut |= tail ? 2 : seg.j0 > 0 ? 1 : 0;
         if (!(ok = seg_publish(bar.ring, rst, rph, seg, lane, abort_flag, ws, 400))) break;
         const int i0 = seg.tile * 2 * T, ntiles = i0 + T < seg.m ? 2 : 1;
         for (int t = 0; ok && t < ntiles; ++t) {
@@ -310,9 +343,22 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
       for (int j = seg.j0; ok && j < seg.j1; ++j) {
         ok = ring.load(walk, j, lane, abort_flag, ws, is_k ? 402 : 404);
         if (j == seg.j0) walk.prefetch();
+        if ((cut & 1) && __all_sync(0xffffffffu, mbar_test_wait(&bar.stored[0], 0))) count_part(0);
       }
     }
     if (ok && is_k) ok = seg_publish(bar.ring, rst, rph, end_segment(), lane, abort_flag, ws, 403);
+    if (ok && (cut & 1) && (ok = warp_wait(&bar.stored[0], 0, abort_flag, ws, 426))) count_part(0);
+    if (ok && (cut & 2)) {
+      if (asks(bar.cut[1]) && (ok = warp_wait(&bar.ask, 0, abort_flag, ws, 427))) {
+        if (lane == 0) {
+          bar.keep = PartCount(bar.cut[1], ws).others();
+          mbar_arrive(&bar.answered);
+        }
+        __syncwarp();
+        if (bar.keep) cut = 0;
+      }
+      if (ok && cut != 0 && (ok = warp_wait(&bar.stored[1], 0, abort_flag, ws, 428))) count_part(1);
+    }
     if (!ok) {
       ring.settle();
       int never = 0;
@@ -493,10 +539,19 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
     constexpr float scale_l2e = Scale<D>::value * kLog2e;
     uint32_t rst = 0, rph = 0;
     // Bits in one register (the passes leave few): parities of the waits for S, O,
-    // the turn, PV and parts; kPending: a P was written whose PV has not been
-    // awaited (SEP_P); kTurned: a block was shared with the other tile before.
-    enum : uint32_t { kS = 1, kO = 2, kTurn = 4, kPv = 8, kParts = 16, kPending = 32, kTurned = 64 };
+    // the turn and PV; kPending: a P was written whose PV has not been
+    // awaited (SEP_P); kTurned: a block was shared with the other tile before; kCut and
+    // 2 kCut: a part of the run's first and last tile was stored; kKept: the last
+    // tile's other parts are there.
+    enum : uint32_t { kS = 1, kO = 2, kTurn = 4, kPv = 8, kPending = 16, kTurned = 32, kCut = 64, kKept = 256 };
     uint32_t bits = 0;
+    // A part holds [tile][4 columns][row]: the lanes of a warp, which own rows,
+    // write and read 512 bytes in a row.
+    constexpr size_t kPart = static_cast<size_t>(256) * D;
+    const size_t mine = static_cast<size_t>(t * 128) * D + (h * (D / 8) * 128 + r) * 4;
+    auto row_of = [&](const Segment& s, const int token, const int of) {
+      return a.o + (static_cast<size_t>(s.start + token) * a.Hq + s.head * G + r - of * G) * D + h * (D / 2);
+    };
     bool ok = true;
     while (ok) {
       Segment seg;
@@ -610,20 +665,22 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
       seg = seg_peek(bar.ring, rst);
       const Shape out = shape(seg);
       const bool holds = out.dual ? t == 0 : seg.j0 < side_end(seg, t);  // this side's O holds a sum
-      const bool whole = seg.j0 == 0 && seg.j1 == seg.blocks;
+      const bool whole = seg.j0 == 0 && seg.j1 == seg.blocks, tail = seg.j1 < seg.blocks;
+      if (tail && asks(seg)) {
+        if (warp == 0 && lane == 0) mbar_arrive(&bar.ask);
+        if (!(ok = warp_wait(&bar.answered, 0, abort_flag, ws, 429))) break;
+        if (bar.keep) bits |= kKept;
+      }
       const int of = r / G, token = seg.tile * 2 * T + t * T + of;
       const bool writes = of < T && token < seg.m;
-      __nv_bfloat16* dst =
-          a.o + (static_cast<size_t>(seg.start + token) * a.Hq + seg.head * G + r - of * G) * D + h * (D / 2);
-      // A part holds [tile][4 columns][row]: the lanes of a warp, which own rows,
-      // write and read 512 bytes in a row.
-      constexpr size_t kPart = static_cast<size_t>(256) * D;
-      const size_t mine = static_cast<size_t>(t * 128) * D + (h * (D / 8) * 128 + r) * 4;
       // This warp's D / 2 columns of O, 32 at a time.
       if (holds) {
         if (!(ok = warp_wait(&bar.o_full[t], (bits & kO) != 0, abort_flag, ws, 424))) break;
         bits ^= kO;
         tc_fence_after();
+      }
+      if (holds && !(bits & kKept)) {
+        __nv_bfloat16* dst = row_of(seg, token, of);
         float* part = a.parts + (2 * blockIdx.x + (seg.j0 == 0)) * kPart + mine;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
@@ -645,47 +702,71 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
           }
         }
       }
-      if (!whole) {
-        if (!(ok = last_part(&bar.stored, &bar.counted, &bar.last, seg, ws, warp, lane, (bits & kParts) != 0, abort_flag,
-                             425)))
-          break;
-        bits ^= kParts;
+      __syncwarp();
+      if (!whole && !(bits & kKept)) {
+        bits |= tail ? 2 * kCut : kCut;
+        if (lane == 0) mbar_arrive(&bar.stored[tail ? 1 : 0]);
       }
-      if (!whole && bar.last && writes) {
-        // The first part lies in its CTA's second place, the others in their
-        // CTA's first. Parts that start past the tile's last block are not there.
-        const int all = math.blocks(seg.m, seg.n, min(token - of + T, seg.m) - 1);
-        int np = 1;
-        while (np <= seg.last_cta - seg.first_cta && part_begin(seg, np, bar.run.per, out.two ? 1 : 0) < all) ++np;
-        const float* from = a.parts + (2 * seg.first_cta + 1) * kPart + mine;
-        for (int c = 0; c < D / 32; ++c, from += 4 * 512) {
-          float4 sum[4];
+      seg_release(bar.ring, rst, rph, lane == 0);
+    }
+
+    // The cut tiles that this CTA adds up: those whose parts it completed.
+    for (int k = 0; ok && k < 2; ++k) {
+      const bool kept = k == 1 && (bits & kKept);
+      if (!kept) {
+        if (!(bits & (kCut << k))) continue;
+        if (!(ok = warp_wait(&bar.counted[k], 0, abort_flag, ws, 425))) break;
+        if (!bar.join[k]) continue;
+      }
+      const Segment seg = bar.cut[k];
+      const Shape sh = shape(seg);
+      const int of = r / G, token = seg.tile * 2 * T + t * T + of;
+      const bool writes = of < T && token < seg.m;
+      __nv_bfloat16* dst = row_of(seg, token, of);
+      // The first part lies in its CTA's second place, or if it was kept in tensor
+      // memory, the others in their CTA's first. Parts that start past the
+      // tile's last block are not there.
+      const int i0 = seg.tile * 2 * T + t * T;
+      const int all = i0 < seg.m ? math.blocks(seg.m, seg.n, min(i0 + T, seg.m) - 1) : 0;
+      int np = 1;
+      while (np <= seg.last_cta - seg.first_cta && part_begin(seg, np, bar.run.per, sh.two ? 1 : 0) < all) ++np;
+      const float* from = a.parts + (2 * seg.first_cta + 1) * kPart + mine;
+      for (int c = 0; c < D / 32; ++c, from += 4 * 512) {
+        float4 sum[4];
+        if (kept) {
+          uint32_t v[16];
+          __syncwarp();
+          tmem_ld16(quad + C::TM_O + t * D + h * (D / 2) + c * 16, v);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            sum[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]), __uint_as_float(v[4 * q + 2]),
+                                 __uint_as_float(v[4 * q + 3]));
+        } else if (writes) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) sum[q] = __ldcg(reinterpret_cast<const float4*>(from + q * 512));
-#pragma unroll 2
-          for (int p = 1; p < np; ++p) {
-            float4 x[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              x[q] = __ldcg(reinterpret_cast<const float4*>(from + (2 * p - 1) * kPart + q * 512));
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              sum[q].x += x[q].x;
-              sum[q].y += x[q].y;
-              sum[q].z += x[q].z;
-              sum[q].w += x[q].w;
-            }
-          }
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            *reinterpret_cast<uint4*>(dst + c * 16 + q * 8) =
-                make_uint4(pack_bf16x2(sum[2 * q].x, sum[2 * q].y), pack_bf16x2(sum[2 * q].z, sum[2 * q].w),
-                           pack_bf16x2(sum[2 * q + 1].x, sum[2 * q + 1].y),
-                           pack_bf16x2(sum[2 * q + 1].z, sum[2 * q + 1].w));
         }
+        if (!writes) continue;
+#pragma unroll 2
+        for (int p = 1; p < np; ++p) {
+          float4 x[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            x[q] = __ldcg(reinterpret_cast<const float4*>(from + (2 * p - 1) * kPart + q * 512));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            sum[q].x += x[q].x;
+            sum[q].y += x[q].y;
+            sum[q].z += x[q].z;
+            sum[q].w += x[q].w;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          *reinterpret_cast<uint4*>(dst + c * 16 + q * 8) =
+              make_uint4(pack_bf16x2(sum[2 * q].x, sum[2 * q].y), pack_bf16x2(sum[2 * q].z, sum[2 * q].w),
+                         pack_bf16x2(sum[2 * q + 1].x, sum[2 * q + 1].y),
+                         pack_bf16x2(sum[2 * q + 1].z, sum[2 * q + 1].w));
       }
-      __syncwarp();
-      seg_release(bar.ring, rst, rph, lane == 0);
     }
   }
 

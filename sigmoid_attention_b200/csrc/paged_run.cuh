@@ -492,11 +492,49 @@ struct TileRing {
   }
 };
 
+// The count of a cut tile's stored parts is one byte in the workspace header, put
+// back to zero by whoever finds it complete.
+struct PartCount {
+  int* word;
+  int shift, parts;
+
+  __device__ __forceinline__ PartCount(const Segment& seg, int* ws)
+      : word(ws + kHdrParts + (seg.first_cta >> 2)), shift(8 * (seg.first_cta & 3)), parts(seg.last_cta - seg.first_cta + 1) {}
+
+  // Counts this CTA's part (whose stores happened before, by a barrier): was it
+  // the last? Released, so that whoever sees this count sees the part, and
+  // acquired, so that whoever is last sees the others' (one instruction: with
+  // fences around a plain atomic this took 3500 cycles).
+  __device__ __forceinline__ bool add() const {
+    unsigned before;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(before) : "l"(word), "r"(1u << shift) : "memory");
+    const bool last = ((before >> shift) & 255u) == static_cast<unsigned>(parts - 1);
+    if (last) clear(parts);
+    return last;
+  }
+
+  // Are the other CTAs' parts all there (and visible)? If so this CTA need not
+  // store its own.
+  __device__ __forceinline__ bool others() const {
+    unsigned now;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(word) : "memory");
+    const bool all = ((now >> shift) & 255u) == static_cast<unsigned>(parts - 1);
+    if (all) clear(parts - 1);
+    return all;
+  }
+
+  __device__ __forceinline__ void clear(int n) const {
+    atomicSub(reinterpret_cast<unsigned*>(word), static_cast<unsigned>(n) << shift);
+  }
+};
+
+// (out of line: two calls)
+static __device__ __noinline__ bool part_count(const Segment& seg, int* ws) { return PartCount(seg, ws).add(); }
+
 // After every epilogue warp of this CTA has stored its share of a tile's
 // part: *last_flag tells whether this CTA's part was the tile's last (uniform over
 // the CTA's epilogue warps; the other parts are then visible). `ph`: parity of
-// the two barriers, flipped by the caller each time. The count of the tile's
-// stored parts is one byte in the workspace header, put back to zero by the last.
+// the two barriers, flipped by the caller each time.
 __device__ __forceinline__ bool last_part(uint64_t* stored, uint64_t* counted, int* last_flag, const Segment& seg,
                                           int* ws, int warp, int lane, uint32_t ph, volatile int* abort_flag, int site) {
   // (The barrier orders every warp's stores before the count.)
@@ -505,17 +543,7 @@ __device__ __forceinline__ bool last_part(uint64_t* stored, uint64_t* counted, i
   if (warp == 0) {
     if (!warp_wait(stored, ph, abort_flag, ws, site)) return false;
     if (lane == 0) {
-      const int parts = seg.last_cta - seg.first_cta + 1;
-      const int shift = 8 * (seg.first_cta & 3);
-      int* word = ws + kHdrParts + (seg.first_cta >> 2);
-      // Released, so that whoever sees this count sees the part, and acquired, so
-      // that whoever is last sees the others' (one instruction: with fences
-      // around a plain atomic this took 3500 cycles).
-      unsigned before;
-      asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(before) : "l"(word), "r"(1u << shift) : "memory");
-      const bool last = ((before >> shift) & 255u) == static_cast<unsigned>(parts - 1);
-      if (last) atomicSub(reinterpret_cast<unsigned*>(word), static_cast<unsigned>(parts) << shift);
-      *last_flag = last;
+      *last_flag = part_count(seg, ws);
       mbar_arrive(counted);
     }
     __syncwarp();
