@@ -705,9 +705,12 @@ int sigattn_fwd_paged(const void* q, long long q_stride, const void* k_cache, co
   const int item = 2 * (128 / G);
   const double units = static_cast<double>(Hkv) * (max_pages * page_size / 128 + 1) * (few ? B : 2.0 * (total / item + B));
   const bool wide = units >= 2147483648.0;
+  const int grid = std::min(info.num_sms, kMaxPagedCtas);
+  const bool spread = static_cast<long long>(Hkv) * (total / (128 / G) + B) <= grid;  // an SM per query tile
+  const int lone = spread ? kLoneUnits * d / 64 : 0;
   const PagedAttend a{static_cast<const bf16*>(q), static_cast<const bf16*>(k_cache), static_cast<const bf16*>(v_cache),
                       static_cast<bf16*>(o), q_stride, cu_seqlens, kv_lens, block_table, B, Hq, Hkv, max_seqlen_q, total,
-                      max_pages, shift, num_pages, d, causal != 0, few ? 1 : 4, few ? kFewCut : kManyCut,
+                      max_pages, shift, num_pages, d, causal != 0, lone, few ? kFewCut : kManyCut,
                       reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes),
                       static_cast<int*>(workspace)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -716,7 +719,6 @@ int sigattn_fwd_paged(const void* q, long long q_stride, const void* k_cache, co
       !make_map(&tk, k_cache, num_pages * Hkv, page_size, d, std::min(page_size, 128)) ||
       !make_map(&tv, v_cache, num_pages * Hkv, page_size, d, std::min(page_size, 128)))
     return map_failure();
-  const int grid = std::min(info.num_sms, kMaxPagedCtas);
   return cuda_status(few ? launch_paged_few(tq, tk, tv, a, wide, grid, s)
                          : launch_paged_many(tq, tk, tv, a, wide, grid, s));
 }

@@ -46,7 +46,7 @@ struct PagedAttend {
   long long q_stride;
   const int *cu, *kv, *table;
   int B, Hq, Hkv, max_q, total, max_pages, page_shift, num_pages, d, causal;
-  int least;     // fewest units of work in a CTA's run (paged_run.cuh)
+  int lone;      // most units per CTA that are shared out by single query tiles (paged_many.cu)
   float cut;     // what a row of a part costs to add up, in units of work
   float* parts;  // partial sums of tiles cut over CTAs, two places per CTA
   int* ws;
@@ -59,6 +59,12 @@ constexpr int kMaxPagedCtas = 152;
 // 44.5 us; and 0 / 2/3 kManyCut / 3 kManyCut: 34 tokens of 7 heads over 29856 keys
 // 84 / 41 / 56 us, 200 tokens of 8 heads over 4000 keys 51 / 37 / 43 us.
 constexpr float kFewCut = 0.02f, kManyCut = 0.003f;
+// PagedAttend::lone, at d = 64. Single tiles against pairs: 200 tokens of 8 heads
+// over 4000 keys 25 / 36 us, 300 tokens of 8 heads 11.8 / 15.7, 500 tokens of 8
+// heads over 5000 keys (d = 128, 16 units) 32 / 42 and over 10000 43 / 53; beyond
+// that a pair's better use of each key block wins: 1000 tokens over 30000 keys 162
+// / 141 us, and at d = 64 500 tokens over 10000 (16 units) 36 / 35, 30000 79 / 65.
+constexpr int kLoneUnits = 16;
 // Query rows per key/value head (G * new tokens) up to which paged_few.cu serves.
 constexpr int kFewRows = 64;
 

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
   grid_dep_wait();
   auto units = [](const SeqInfo& s) -> U { return seq_blocks(s.n); };
   auto joins = [&](const SeqInfo& s) { return a.cut * static_cast<float>(s.m * G) * seq_blocks(s.n); };
-  if (a.B > kWarpPlan) plan_run<C::THREADS>(a, &bar.run, units, joins);
+  if (a.B > kWarpPlan) plan_run<C::THREADS>(a, 1, &bar.run, units, joins);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     // Both walk the run; the K warp hands its segments to the other roles.
     const bool is_k = warp == kLoadK;
     const OneTile tiles{};
-    const PlanRun<U> run = a.B > kWarpPlan ? bar.run : plan_warp<U>(a, units, joins);
+    const PlanRun<U> run = a.B > kWarpPlan ? bar.run : plan_warp<U>(a, 1, units, joins);
     RunWalker<U, OneTile> walk(a, tiles, run, lane);
     const Segment& seg = walk.seg;
     TileRing<D> ring{is_k ? &tm_k : &tm_v, smem + (is_k ? 0 : C::KST * C::TILE_BYTES), bar.full + (is_k ? 0 : C::KST),

@@ -121,14 +121,19 @@ __device__ __forceinline__ U floor_sum(uint32_t n, uint32_t x, uint32_t y) {
 }
 
 // A sequence's tiles: an item is two query tiles, 2 T tokens (the last may be
-// one). A block of an item is as many units as it has tiles: two tiles' products
-// bound a block, one tile's are about as fast as its keys arrive, in half the
-// time.
+// one), or one tile where the call has few and short ones (kLoneUnits): more CTAs
+// then share the tiles, their parts and the adding up of these, at the cost of
+// loading each key block once per tile. A block of an item is as many units as it
+// has tiles: two tiles' products bound a block, one tile's are about as fast as its
+// keys arrive, in half the time.
 struct TileMath {
   int T;
+  int pairs;  // items of two tiles
   int causal;
-  __device__ __forceinline__ int items(const SeqInfo& s) const { return (s.m + 2 * T - 1) / (2 * T); }
-  __device__ __forceinline__ bool two(const SeqInfo& s, int k) const { return k * 2 * T + T < s.m; }
+  __device__ __forceinline__ int item() const { return T << pairs; }
+  __device__ __forceinline__ int items(const SeqInfo& s) const { return (s.m + item() - 1) / item(); }
+  __device__ __forceinline__ bool two(int m, int k) const { return pairs && k * 2 * T + T < m; }
+  __device__ __forceinline__ bool two(const SeqInfo& s, int k) const { return two(s.m, k); }
   __device__ __forceinline__ int shift(const SeqInfo& s, int k) const { return two(s, k) ? 1 : 0; }
   // Keys that token i sees.
   __device__ __forceinline__ int seen(int m, int n, int i) const {
@@ -137,7 +142,7 @@ struct TileMath {
   // Blocks that tokens up to i of the chunk walk.
   __device__ __forceinline__ int blocks(int m, int n, int i) const { return seq_blocks(seen(m, n, i)); }
   __device__ __forceinline__ int blocks(const SeqInfo& s, int k) const {
-    return blocks(s.m, s.n, min((k + 1) * 2 * T, s.m) - 1);
+    return blocks(s.m, s.n, min((k + 1) * item(), s.m) - 1);
   }
   // Units of items 0 .. k - 1 (k <= items).
   template <typename U>
@@ -147,12 +152,12 @@ struct TileMath {
       --k;
       sum = static_cast<U>(seq_blocks(s.n)) << shift(s, k);
     }
-    if (!causal) return sum + 2 * static_cast<U>(k) * seq_blocks(s.n);
+    if (!causal) return sum + (static_cast<U>(k) * seq_blocks(s.n) << pairs);
     // Item i's last token sees n - m + (i + 1) 2 T keys, or (more rows than
     // tokens) none: then it still walks the block that writes its zeros.
-    const int item = 2 * T, c = s.n - s.m;
+    const int item = this->item(), c = s.n - s.m;
     const int none = c < 0 ? min(k, -c / item) : 0;
-    return sum + 2 * (static_cast<U>(none) + floor_sum<U>(k - none, item, c + (none + 1) * item + kKeyBlock - 1));
+    return sum + ((static_cast<U>(none) + floor_sum<U>(k - none, item, c + (none + 1) * item + kKeyBlock - 1)) << pairs);
   }
 };
 
@@ -260,22 +265,31 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
   if (lane == 0 && warp == kLoadV) tma_prefetch_desc(&tm_v);
   const int G = a.Hq / a.Hkv;
   const int T = 128 / G;  // tokens per tile
-  const TileMath math{T, a.causal};
+  TileMath math{T, a.lone == 0, a.causal};
   grid_dep_launch();
   grid_dep_wait();
   auto units = [&](const SeqInfo& s) { return math.before<U>(s, math.items(s)); };
   auto joins = [&](const SeqInfo& s) {
     const float tiles = math.two(s, 0) ? 2.0f : 1.0f;
-    return a.cut * tiles * tiles * static_cast<float>(min(s.m, 2 * T) * G) * seq_blocks(s.n);
+    return a.cut * 2.0f * tiles * static_cast<float>(min(s.m, math.item()) * G) * seq_blocks(s.n);
   };
-  if (a.B > kWarpPlan) plan_run<C::THREADS>(a, &bar.run, units, joins);
+  // Single tiles where that is at most a.lone units per CTA, else pairs.
+  auto settled = [&](U total) { return math.pairs || total <= static_cast<U>(a.lone) * gridDim.x; };
+  if (a.B > kWarpPlan) {
+    for (;; math.pairs = 1) {
+      plan_run<C::THREADS>(a, 1 << math.pairs, &bar.run, units, joins);
+      if (math.pairs) break;
+      __syncthreads();
+      if (settled(bar.run.total)) break;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem_base;
 
   auto shape = [&](const Segment& seg) {
-    const bool two = seg.tile * 2 * T + T < seg.m;
+    const bool two = math.two(seg.m, seg.tile);
     return Shape{two, !two && seg.j1 - seg.j0 > 1};
   };
   // Does the CTA of a tile's first part look whether the rest is there before it
@@ -285,8 +299,8 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
   // Side t of a segment that is not dual works on blocks [j0, end): none where
   // its tile has no tokens or its rows see none of them.
   auto side_end = [&](const Segment& seg, int t) {
-    const int i0 = seg.tile * 2 * T + t * T;
-    if (i0 >= seg.m) return seg.j0;
+    const int i0 = seg.tile * math.item() + t * T;
+    if (t == 1 && !math.two(seg.m, seg.tile)) return seg.j0;
     return max(seg.j0, min(seg.j1, math.blocks(seg.m, seg.n, min(i0 + T, seg.m) - 1)));
   };
 
@@ -294,8 +308,19 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
     // ------------------------------------- producers: segments, Q and K; V
     // Both walk the run; the K warp hands its segments to the other roles.
     const bool is_k = warp == kLoadK;
-    const PlanRun<U> run = a.B > kWarpPlan ? bar.run : plan_warp<U>(a, units, joins);
-    if (is_k && lane == 0) bar.run.per = run.per;  // (read by the epilogue once it has a segment)
+    PlanRun<U> run;
+    if (a.B > kWarpPlan) {
+      run = bar.run;
+    } else {
+      for (;; math.pairs = 1) {
+        run = plan_warp<U>(a, 1 << math.pairs, units, joins);
+        if (settled(run.total)) break;
+      }
+    }
+    if (is_k && lane == 0) {  // (read by the other roles once they have a segment)
+      bar.run.per = run.per;
+      bar.run.pairs = math.pairs;
+    }
     RunWalker<U, TileMath> walk(a, math, run, lane);
     const Segment& seg = walk.seg;
     TileRing<D> ring{is_k ? &tm_k : &tm_v, is_k ? sK : sV, is_k ? bar.k_full : bar.v_full, is_k ? bar.k_empty : bar.v_empty,
@@ -326,7 +351,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         if (lane == 0 && (tail || seg.j0 > 0)) bar.cut[tail ? 1 : 0] = seg;
         cut |= tail ? 2 : seg.j0 > 0 ? 1 : 0;
         if (!(ok = seg_publish(bar.ring, rst, rph, seg, lane, abort_flag, ws, 400))) break;
-        const int i0 = seg.tile * 2 * T, ntiles = i0 + T < seg.m ? 2 : 1;
+        const int i0 = seg.tile * math.item(), ntiles = math.two(seg.m, seg.tile) ? 2 : 1;
         for (int t = 0; ok && t < ntiles; ++t) {
           if (!(ok = warp_wait(&bar.q_empty[qst], qph ^ 1, abort_flag, ws, 401))) break;
           if (lane == 0) {
@@ -398,6 +423,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         if (!(ok = seg_read<false>(bar.ring, rst, rph, &seg, abort_flag, ws, 410))) break;
         seg_release(bar.ring, rst, rph, true);
         if (seg.j1 < 0) break;
+        math.pairs = bar.run.pairs;
         const Shape sh = shape(seg);
         const int end = side_end(seg, t);
         const int len = seg.j1 - seg.j0;
@@ -557,8 +583,9 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
       Segment seg;
       if (!(ok = seg_read<true>(bar.ring, rst, rph, &seg, abort_flag, ws, 420))) break;
       if (seg.j1 < 0) break;
+      math.pairs = bar.run.pairs;
       const Shape sh = shape(seg);
-      const int i0 = seg.tile * 2 * T + (sh.dual ? 0 : t * T);
+      const int i0 = seg.tile * math.item() + (sh.dual ? 0 : t * T);
       // This side's blocks: from `j` on, every `step`-th, below `end`. Blocks below
       // `joint_end` are shared with the other tile.
       const int step = sh.dual ? 2 : 1;
@@ -671,8 +698,8 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         if (!(ok = warp_wait(&bar.answered, 0, abort_flag, ws, 429))) break;
         if (bar.keep) bits |= kKept;
       }
-      const int of = r / G, token = seg.tile * 2 * T + t * T + of;
-      const bool writes = of < T && token < seg.m;
+      const int of = r / G, token = seg.tile * math.item() + t * T + of;
+      const bool writes = (t == 0 || out.two) && of < T && token < seg.m;
       // This warp's D / 2 columns of O, 32 at a time.
       if (holds) {
         if (!(ok = warp_wait(&bar.o_full[t], (bits & kO) != 0, abort_flag, ws, 424))) break;
@@ -720,14 +747,14 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
       }
       const Segment seg = bar.cut[k];
       const Shape sh = shape(seg);
-      const int of = r / G, token = seg.tile * 2 * T + t * T + of;
-      const bool writes = of < T && token < seg.m;
+      const int of = r / G, token = seg.tile * math.item() + t * T + of;
+      const bool writes = (t == 0 || sh.two) && of < T && token < seg.m;
       __nv_bfloat16* dst = row_of(seg, token, of);
       // The first part lies in its CTA's second place, or if it was kept in tensor
       // memory, the others in their CTA's first. Parts that start past the
       // tile's last block are not there.
-      const int i0 = seg.tile * 2 * T + t * T;
-      const int all = i0 < seg.m ? math.blocks(seg.m, seg.n, min(i0 + T, seg.m) - 1) : 0;
+      const int i0 = seg.tile * math.item() + t * T;
+      const int all = writes ? math.blocks(seg.m, seg.n, min(i0 + T, seg.m) - 1) : 0;
       int np = 1;
       while (np <= seg.last_cta - seg.first_cta && part_begin(seg, np, bar.run.per, sh.two ? 1 : 0) < all) ++np;
       const float* from = a.parts + (2 * seg.first_cta + 1) * kPart + mine;

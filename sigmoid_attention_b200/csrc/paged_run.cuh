@@ -72,22 +72,23 @@ struct PlanRun {
   U rem;
   SeqInfo s;
   int b, count, per;
+  int pairs;  // (paged_many.cu)
+  U total;
 };
 
-// How long the runs are: an equal share, at least a.least units, and by what the
+// How long the runs are: an equal share, at least `least` units, and by what the
 // parts take to add up; 0 (and an error) beyond any call that could end.
 template <typename U>
-__device__ __forceinline__ U run_length(const PagedAttend& a, U total, float join) {
-  const U per = max(static_cast<U>(sqrtf(join)),
-                    max(static_cast<U>(a.least), (total + gridDim.x - 1) / gridDim.x));
+__device__ __forceinline__ U run_length(const PagedAttend& a, int least, U total, float join) {
+  const U per = max(static_cast<U>(sqrtf(join)), max(static_cast<U>(least), (total + gridDim.x - 1) / gridDim.x));
   if (per <= INT_MAX) return per;
   if (blockIdx.x == 0) raise_invalid(a.ws, 206);
   return 0;
 }
 
 // units(s): units of one key/value head of a sequence with new tokens. Runs are
-// at least a.least units long (at least a block's, so that a tile's CTAs all
-// have a block of it). U: an unsigned type that holds the call's units; the
+// at least `least` units long (a block's, so that a tile's CTAs all have a block
+// of it). U: an unsigned type that holds the call's units; the
 // usual 32 bits make this half as long as 64.
 // join(s): how long the parts of the sequence's largest tile take to add up, if
 // cut at every unit, in units of work. A tile of b units cut into runs of x
@@ -96,7 +97,7 @@ __device__ __forceinline__ U run_length(const PagedAttend& a, U total, float joi
 // their last CTA can add up in the time the cut saves.
 // Ends before the caller's next barrier; every thread of the CTA takes part.
 template <int THREADS, typename U, typename Units, typename Join>
-__device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun<U>* run, Units units, Join join) {
+__device__ __forceinline__ void plan_run(const PagedAttend& a, int least, PlanRun<U>* run, Units units, Join join) {
   constexpr int kWarps = THREADS / 32;
   static_assert(THREADS % 32 == 0 && kWarps <= 32, "whole warps");
   __shared__ U sums[kWarps];
@@ -140,12 +141,13 @@ __device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun<U>* run, 
   const U before = __shfl_sync(0xffffffffu, upto, warp > 0 ? warp - 1 : 0);
   const U base = (warp > 0 ? before : 0) + incl - mine;
   const float all_join = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < kWarps ? joins[lane] : 0));
-  const U per = run_length<U>(a, total, all_join);
+  const U per = run_length<U>(a, least, total, all_join);
   const U left = per > 0 ? total : 0;
   const U first = min(left, per * blockIdx.x);
   if (tid == 0) {
     run->count = static_cast<int>(min(per, left - first));
     run->per = static_cast<int>(per);
+    run->total = total;
   }
   if (first >= base && first - base < mine) {
     U rem = first - base;
@@ -167,7 +169,7 @@ __device__ __forceinline__ void plan_run(const PagedAttend& a, PlanRun<U>* run, 
 // batch of 108 took 11.8 instead of 11.1 us).
 constexpr int kWarpPlan = 32;
 template <typename U, typename Units, typename Join>
-__device__ __forceinline__ PlanRun<U> plan_warp(const PagedAttend& a, Units units, Join join) {
+__device__ __forceinline__ PlanRun<U> plan_warp(const PagedAttend& a, int least, Units units, Join join) {
   const int lane = threadIdx.x & 31;
   PlanRun<U> run;
   SeqInfo s;
@@ -189,9 +191,10 @@ __device__ __forceinline__ PlanRun<U> plan_warp(const PagedAttend& a, Units unit
     if (lane >= o) incl += u;
   }
   const U total = __shfl_sync(0xffffffffu, incl, 31);
-  const U per = run_length<U>(a, total, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(longest))));
+  const U per = run_length<U>(a, least, total, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(longest))));
   const U left = per > 0 ? total : 0, first = min(left, per * blockIdx.x);
   run.per = static_cast<int>(per);
+  run.total = total;
   run.count = static_cast<int>(min(per, left - first));
   // The sequence that the run starts in.
   const U base = incl - mine;
