@@ -26,8 +26,8 @@
 //    that all of them add to one O in order.
 //
 // Roles (20 warps): 0-15 epilogue (warps 0-7 tile 0, 8-15 tile 1; per tile, four
-// warps for every other 32 of a block's keys), 16 and 17 the producers of K (and Q) and
-// of V, 18 and 19 the issuers of tiles 0 and 1.
+// warps for every other 32 of a block's keys), 16 and 17 the producers of K and
+// of Q and V, 18 and 19 the issuers of tiles 0 and 1.
 // TMEM: S of tile t at columns [128t, 128t + 128), O at 256 + t D; P over S
 // (d = 128) or in a region of its own after O (d = 64).
 #include "paged_run.cuh"
@@ -258,11 +258,11 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
     tmem_alloc(&bar.tmem_base, C::TMEM_COLS);
     tmem_relinquish();
   }
-  if (lane == 0 && warp == kLoadK) {
+  if (lane == 0 && warp == kLoadK) tma_prefetch_desc(&tm_k);
+  if (lane == 0 && warp == kLoadV) {
     tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
   }
-  if (lane == 0 && warp == kLoadV) tma_prefetch_desc(&tm_v);
   const int G = a.Hq / a.Hkv;
   const int T = 128 / G;  // tokens per tile
   TileMath math{T, a.lone == 0, a.causal};
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
   };
 
   if (warp == kLoadK || warp == kLoadV) {
-    // ------------------------------------- producers: segments, Q and K; V
+    // ------------------------------------- producers: segments and K; Q and V
     // Both walk the run; the K warp hands its segments to the other roles.
     const bool is_k = warp == kLoadK;
     PlanRun<U> run;
@@ -351,6 +351,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         if (lane == 0 && (tail || seg.j0 > 0)) bar.cut[tail ? 1 : 0] = seg;
         cut |= tail ? 2 : seg.j0 > 0 ? 1 : 0;
         if (!(ok = seg_publish(bar.ring, rst, rph, seg, lane, abort_flag, ws, 400))) break;
+      } else {  // (here, since V is needed last)
         const int i0 = seg.tile * math.item(), ntiles = math.two(seg.m, seg.tile) ? 2 : 1;
         for (int t = 0; ok && t < ntiles; ++t) {
           if (!(ok = warp_wait(&bar.q_empty[qst], qph ^ 1, abort_flag, ws, 401))) break;
