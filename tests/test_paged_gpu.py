@@ -416,6 +416,29 @@ def test_attend_chunks(Hq, Hkv, d, ps, q, kv, causal):
     b.check(o, causal)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Hq, Hkv, d, ps, q, kv", [
+    # pairs of query tiles: more tiles than SMs, up to 32 sequences and more
+    (48, 48, 64, 32, [700, 1, 300], [900, 2000, 300]), (64, 16, 128, 64, [300, 40, 1], [800, 3000, 500]),
+    (48, 16, 64, 16, [130, 85, 84], [130, 1000, 84]), (24, 24, 128, 128, [129, 257, 640], [2000, 300, 640]),
+    (8, 8, 64, 16, [7 + 13 * i % 200 for i in range(40)], [250 + 17 * i for i in range(40)]),
+    (8, 4, 128, 64, [1 + 31 * i % 90 for i in range(70)], [90 + 5 * i for i in range(70)]),
+    # few tiles over texts so long that pairs are taken all the same
+    (2, 2, 64, 128, [300, 100], [80000, 300]), (2, 1, 128, 256, [200, 65], [500000, 250000]),
+    (1, 1, 64, 256, [100, 65] + [1] * 32, [300000, 120000] + [9] * 32),
+    # few short tiles in more than 32 sequences
+    (1, 1, 128, 16, [1 + 29 * i % 80 for i in range(40)], [80 + 11 * i for i in range(40)]),
+])
+def test_attend_shared_out(Hq, Hkv, d, ps, q, kv, causal):
+    """Query tiles shared out in pairs or singly, planned by a warp or the CTA."""
+    b = Batch(q, kv, Hq, Hkv, d, ps, seed=len(q) + Hq)
+    o = b.run(causal)
+    b.fine()
+    b.check(o, causal)
+    for _ in range(3):
+        assert torch.equal(o, b.run(causal))
+
+
 @pytest.mark.parametrize("Hq, Hkv, d, m", [(8, 2, 64, 1), (8, 8, 128, 1), (4, 2, 128, 40), (16, 1, 64, 700)])
 def test_attend_long_text(Hq, Hkv, d, m):
     """Keys cut over many SMs, weights far in the tail."""
