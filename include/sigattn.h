@@ -353,7 +353,8 @@ SIGATTN_API size_t sigattn_paged_workspace_size(int Hq, int Hkv, int d, int max_
  *    bounds are out of order or out of [0, total], gets no work: its rows are
  *    left untouched and the error word is raised (site -(b+1)).
  *  - A page number outside [0, num_pages) among a sequence's pages contributes
- *    nothing to its sums and raises site 203.
+ *    nothing to its sums and raises site 203. A batch of more than 2^31 key
+ *    blocks (128 keys of one query tile) per SM gets no work and raises site 206.
  *  - Cached values of tokens < kv_lens[b] must be finite; whatever else the
  *    pages hold (NaN included) changes no result.
  *  - The keys are cut over the SMs where that balances the work, and the

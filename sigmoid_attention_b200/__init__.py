@@ -599,13 +599,15 @@ class PagedCache:
 
     def release(self, keep_lens=None) -> None:
         """Keep the first keep_lens[b] tokens of every sequence (None: none)
-        and give the other pages back."""
+        and give the other pages back. If a sequence holds fewer than that,
+        nothing changes and the error word is raised."""
         sigattn_paged_release(self.lens, keep_lens, self.block_table, self.free_pages, self.free_count, self.free_count,
                               self.page_size, self.workspace)
         if keep_lens is None:
             self.lens.zero_()
         else:
-            self.lens.copy_(keep_lens)
+            met = ((keep_lens >= 0) & (keep_lens <= self.lens)).all()
+            self.lens.copy_(torch.where(met, keep_lens, self.lens))
 
     def check(self) -> None:
         """Synchronise and raise if a call reported a problem on the device."""

@@ -448,6 +448,32 @@ def test_attend_long_text(Hq, Hkv, d, m):
     b.check(o, True)
 
 
+@pytest.mark.parametrize("B, m", [(4096, 1), (2000, 1), (1200, 70)])
+def test_attend_large_batches(B, m):
+    """Many short sequences, every fourth without new tokens."""
+    b = Batch([0 if i % 4 == 2 else 1 + i % m for i in range(B)], [m + i % 37 for i in range(B)], 2, 1, 64, 16, seed=B)
+    o = b.run(True)
+    b.fine()
+    assert bool(o.isfinite().all())
+    for s in list(range(0, B, 97)) + [B - 1]:
+        if b.q_lens[s]:
+            ref, A = b.exact(s, True)
+            at = int(b.cu[s])
+            err = (o[at:at + b.q_lens[s]].double() - ref).abs()
+            inner = (2.0 ** -8 + 1e-3 + b.kv_lens[s] * 2.0 ** -23) * A
+            assert bool((err <= inner + 2.0 ** -8 * (ref.abs() + inner)).all())
+
+
+@pytest.mark.parametrize("most", [16, 17, 100, 5000, 1 << 24])
+def test_attend_larger_bounds_on_new_tokens(most):
+    """max_seqlen_q only has to be large enough."""
+    b = Batch([1, 3, 1], [700, 3, 3000], 8, 2, 128, 32)
+    b.ws = workspace(sa.sigattn_paged_workspace_size(8, 2, 128, most))
+    o = b.run(True, max_q=most)
+    b.fine()
+    b.check(o, True)
+
+
 def test_attend_rows_that_see_nothing():
     """More rows than tokens: rows before position 0 are zero (causal), and a
     sequence without tokens gives zeros either way."""
@@ -713,3 +739,27 @@ def test_steps_equal_the_whole_prompt(Hq, Hkv, d):
     cache.release()
     assert int(cache.free_count) == 64 and sorted(cache.free_pages.tolist()) == list(range(64))
     cache.check()
+
+
+def test_cache_survives_a_refused_release():
+    """A release of more tokens than there are changes nothing, a step that needs
+    more pages than are free stores nothing, and the cache goes on."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    normal = lambda n, h: torch.randn(n, h, 64, generator=g, device=DEV).to(torch.bfloat16)  # noqa: E731
+    cache, other = (sa.PagedCache(6, 16, 4, 2, 64, 2, 4, max_new=64) for _ in range(2))
+    first, second = [(normal(n, 4), normal(n, 2), normal(n, 2)) for n in (50, 5)]
+    for c in (cache, other):
+        c.step(*first, i32([20, 30]))
+        c.check()
+    cache.release(i32([3, 31]))
+    with pytest.raises(sa.SigattnError, match="-2"):
+        cache.check()
+    assert cache.lens.tolist() == [20, 30] and int(cache.free_count) == 2
+    o = cache.step(normal(60, 4), normal(60, 2), normal(60, 2), i32([30, 30]))
+    with pytest.raises(sa.SigattnError, match="202"):
+        cache.check()
+    assert bool((o == 0).all()) and cache.lens.tolist() == [20, 30]
+    assert torch.equal(cache.step(*second, i32([4, 1])), other.step(*second, i32([4, 1])))
+    cache.release(i32([1, 0]))
+    cache.check()
+    assert cache.lens.tolist() == [1, 0] and int(cache.free_count) == 5
