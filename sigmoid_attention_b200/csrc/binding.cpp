@@ -2,7 +2,7 @@
 //
 // A serving step makes a few calls per layer whose kernels take 3 to 10 us. Checked
 // in Python and marshalled by ctypes such a call took 8 to 12 us on the host, so
-// the host set the pace; here it takes about 4 us, most of it the launch. Each
+// the host set the pace; here it takes about 3 us, most of it the launch. Each
 // function checks its tensors (type, device, shape, strides), takes the current
 // stream unless one is given, and calls the C function of the same name; the
 // names and argument order are those of the package's Python functions.

@@ -56,8 +56,10 @@ struct PagedAttend {
 constexpr int kMaxPagedCtas = 152;
 // PagedAttend::cut. Measured, per setting 0 / kFewCut / 5 kFewCut: one token of 8
 // query rows over 36663 keys 25.7 / 16.4 / 19.1 us, of 16 over 131072 52.4 / 36.3 /
-// 44.5 us; and 0 / 2/3 kManyCut / 3 kManyCut: 34 tokens of 7 heads over 29856 keys
-// 84 / 41 / 56 us, 200 tokens of 8 heads over 4000 keys 51 / 37 / 43 us.
+// 44.5 us; per 1/2 / 1 / 2 / 4 kManyCut: 200 tokens of 8 heads over 4000 keys 26.9 /
+// 25.2 / 26.7 / 28.1 us, 200 of one head over 60000 58.7 / 56.2 / 58.6 / 68.5, 700 of
+// 4 heads over 1500 23.8 / 21.4 / 21.5 / 22.7 (and 0 in pairs: 34 tokens of 7 heads
+// over 29856 keys 84 us, with it 41).
 constexpr float kFewCut = 0.02f, kManyCut = 0.003f;
 // PagedAttend::lone, at d = 64. Single tiles against pairs: 200 tokens of 8 heads
 // over 4000 keys 25 / 36 us, 300 tokens of 8 heads 11.8 / 15.7, 500 tokens of 8

@@ -6,8 +6,8 @@
 // its run itself (plan_run: a prefix sum over the batch's lengths), its
 // producer walks it and hands every segment (the part of one tile's blocks
 // that lies in the run) to the other roles through a ring in shared memory.
-// A tile whose blocks lie in several CTAs is joined by the CTA that stores
-// its part last (last_part).
+// A tile whose blocks lie in several CTAs is joined by the CTA that counts
+// its part last (PartCount).
 // Blocks are 1 or 2 units long (a block for one query tile or for two); a block
 // belongs to the CTA in whose run its first unit lies. (Units of keys, so that
 // texts' last blocks count by their keys, were tried: a short block takes as
