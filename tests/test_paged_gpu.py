@@ -576,6 +576,17 @@ def test_attend_bad_sequences_get_no_work(long):
         assert bool(o[~keep].isnan().all())
 
 
+@pytest.mark.parametrize("q", [[1, 2, 1], [150, 90, 1]])
+def test_attend_shared_pages(q):
+    """Sequences that share a prefix's pages, and a page twice in one text."""
+    b = Batch(q, [400, 300, 333], 8, 2, 64, 32)
+    b.table[1, :5] = b.table[0, :5]
+    b.table[2, 3:6] = b.table[0, 7]
+    o = b.run(True)
+    b.fine()
+    b.check(o, True)
+
+
 def test_attend_far_pages():
     """Offsets past 32 bits: a cache of more than 2^31 elements (and more than
     2^32 bytes), used at both ends."""
