@@ -72,6 +72,11 @@ __device__ __forceinline__ bool last_reader(int* ws) {
 
 }  // namespace
 
+// AHEAD: a call of one CTA and of no more sequences than threads. The pages that the
+// sequences go on in and the stack's top are then loaded while the sums are
+// formed: 64 single tokens 4.1 -> 3.6 us. (In larger calls and for released pages it
+// is no gain: 256 prompts 5.7 -> 5.9 us, tails of 64 sequences 3.3 either way.)
+template <bool AHEAD>
 __global__ void __launch_bounds__(kThreads) reserve_kernel(PagedReserve a) {
   grid_dep_launch();
   grid_dep_wait();
@@ -81,6 +86,8 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(PagedReserve a) {
   int* s_cached = smem_pages;          // [B] tokens before the call
   int* s_cu = s_cached + a.B;          // [B + 1] new tokens before sequence b
   int* s_pg = s_cu + a.B + 1;          // [B + 1] new pages before sequence b
+  __shared__ int s_page[AHEAD ? kThreads : 1];   // the page that sequence b goes on in
+  __shared__ int s_stack[AHEAD ? kThreads : 1];  // the stack's top pages
   const int tid = threadIdx.x;
   const int sh = a.page_shift, ps = 1 << sh;
   const int most = a.max_pages << sh;
@@ -94,6 +101,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(PagedReserve a) {
   uint32_t tok = 0, pg = 0;
   float tokens = 0.f;  // so many that 32 bits would not hold them show here
   int worst = a.B;
+  int page0 = -1, top = -1;
   for (int b = b0; b < b1; ++b) {
     const int c = a.cached[b], m = a.fresh[b];
     s_cached[b] = c;
@@ -104,9 +112,11 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(PagedReserve a) {
       tok += m;
       tokens += m;
       pg += pages_of(c + m, sh) - pages_of(c, sh);
+      if (AHEAD && m > 0 && (c & (ps - 1)) != 0) page0 = a.table[static_cast<size_t>(b) * a.max_pages + (c >> sh)];
     }
   }
   __syncthreads();
+  if (AHEAD && s_count <= a.num_pages && tid < s_count) top = a.free_pages[s_count - 1 - tid];
   if (worst < a.B) atomicMin(&s_bad, worst);
   if (tokens > 1e6f) atomicAdd(&s_tokens, tokens);
   uint32_t total_tok, total_pg;
@@ -129,6 +139,10 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(PagedReserve a) {
   if (tid == 0) {
     s_cu[a.B] = T;
     s_pg[a.B] = P;
+  }
+  if (AHEAD) {
+    s_page[tid] = page0;
+    s_stack[tid] = top;
   }
   __syncthreads();
   if (s_last) {
@@ -167,7 +181,11 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(PagedReserve a) {
         if (k != seen) {
           seen = k;
           int* entry = a.table + static_cast<size_t>(b) * a.max_pages + k;
-          page = k < have ? *entry : a.free_pages[count - 1 - (s_pg[b] + k - have)];
+          const int i = s_pg[b] + k - have;  // which new page
+          if (AHEAD && (k < have || i < kThreads))
+            page = k < have ? s_page[b] : s_stack[i];
+          else
+            page = k < have ? *entry : a.free_pages[count - 1 - i];
           if (page < 0 || page >= a.num_pages) {
             raise_invalid(a.ws, 203);
             page = -1;
@@ -259,7 +277,7 @@ constexpr int kPagesSmem = (3 * kMaxBatch + 2) * static_cast<int>(sizeof(int));
 cudaError_t pages_setup() {
   static PerDeviceOnce attr;
   return attr.run([] {
-    const cudaError_t e = cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPagesSmem);
+    const cudaError_t e = cudaFuncSetAttribute(reserve_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPagesSmem);
     return e != cudaSuccess ? e
                             : cudaFuncSetAttribute(release_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPagesSmem);
   });
@@ -273,7 +291,8 @@ cudaError_t launch_paged_reserve(const PagedReserve& a, int num_sms, cudaStream_
   const int smem = (3 * a.B + 2) * static_cast<int>(sizeof(int));
   const long long work = static_cast<long long>(a.rows) / 4 + 1;
   const int grid = static_cast<int>(std::max<long long>(1, std::min<long long>(2 * num_sms, (work + kThreads - 1) / kThreads)));
-  return launch_programmatic(reserve_kernel, dim3(grid), dim3(kThreads), smem, stream, a);
+  return launch_programmatic(grid == 1 && a.B <= kThreads ? reserve_kernel<true> : reserve_kernel<false>, dim3(grid),
+                             dim3(kThreads), smem, stream, a);
 }
 
 cudaError_t launch_paged_release(const PagedRelease& a, int num_sms, cudaStream_t stream) {
