@@ -42,7 +42,7 @@
 // stored, counted, added up).
 //
 // Roles (17 warps): 0-7 weights, four per group (thread = key), 8-11 output
-// (thread = column of O), 12 and 13 the producers of K (and Q) and of V, 14 the
+// (thread = column of O), 12 and 13 the producers of K and of Q and V, 14 the
 // issuer of S^T, 15 and 16 the groups' issuers of O^T.
 #include "paged_run.cuh"
 
@@ -64,10 +64,11 @@ struct FewCfg {
   static constexpr int STAGES = KST + VST;
   static constexpr int Q_CHUNK = NR * 128;
   static constexpr int Q_BYTES = CH * Q_CHUNK;
+  static constexpr int QST = NR == 16 ? 4 : 2;          // segments' queries loaded ahead
   static constexpr int P_BYTES = kKeyBlock * 128;      // rows of 64 columns, NR of them in use
   static constexpr int OFF_P = STAGES * TILE_BYTES;
   static constexpr int OFF_Q = OFF_P + 2 * P_BYTES;
-  static constexpr int OFF_RED = OFF_Q + 2 * Q_BYTES;   // slices' sums of four rows of a join
+  static constexpr int OFF_RED = OFF_Q + QST * Q_BYTES;   // slices' sums of four rows of a join
   static constexpr int LPR = D / 4, SUB = 32 / LPR;     // lanes per row of a part, rows a warp reads at once
   static constexpr int OUT_WARPS = 4;
   static constexpr int SLICES = OUT_WARPS * SUB, RC = 4;
@@ -93,10 +94,10 @@ struct OneTile {
   }
 };
 
-template <int STAGES, typename U>
+template <int STAGES, int QST, typename U>
 struct FewBarriers {
   uint64_t full[STAGES], empty[STAGES];  // K slots first, then V slots
-  uint64_t q_full[2], q_empty[2];
+  uint64_t q_full[QST], q_empty[QST];
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full[2], p_empty[2];
   uint64_t o_full[2], o_empty[2];
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
                      const __grid_constant__ CUtensorMap tm_v, const PagedAttend a) {
   using C = FewCfg<D, NR>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ FewBarriers<C::STAGES, U> bar;
+  __shared__ FewBarriers<C::STAGES, C::QST, U> bar;
   __shared__ float s_log2n[C::EPI_WARPS][NR];  // each epilogue warp's log2 N and N of the segment's rows
   __shared__ int s_seen[C::EPI_WARPS][NR];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -136,8 +137,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
       for (int s = 0; s < C::STAGES; ++s) mbar_init(&bar.empty[s], s < C::KST ? 1 : 2);
     } else if (warp < 4) {
       const int s = warp - 2;
-      mbar_init(&bar.q_full[s], 1);
-      mbar_init(&bar.q_empty[s], 1);
+      for (int i = s; i < C::QST; i += 2) { mbar_init(&bar.q_full[i], 1); mbar_init(&bar.q_empty[i], 1); }
       mbar_init(&bar.s_full[s], 1);
       mbar_init(&bar.s_empty[s], 4);
       mbar_init(&bar.p_full[s], 4);
@@ -157,16 +157,18 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     tmem_alloc(&bar.tmem_base, C::TMEM_COLS);
     tmem_relinquish();
   }
-  if (lane == 0 && warp == kLoadK) {
+  if (lane == 0 && warp == kLoadK) tma_prefetch_desc(&tm_k);
+  if (lane == 0 && warp == kLoadV) {
     tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
   }
-  if (lane == 0 && warp == kLoadV) tma_prefetch_desc(&tm_v);
   const int G = a.Hq / a.Hkv;
   grid_dep_launch();
   grid_dep_wait();
   auto units = [](const SeqInfo& s) -> U { return seq_blocks(s.n); };
   auto joins = [&](const SeqInfo& s) { return a.cut * static_cast<float>(s.m * G) * seq_blocks(s.n); };
+  SeqWords words{};
+  if (a.B <= kWarpPlan && (warp == kLoadK || warp == kLoadV)) words = seq_load(a, lane);
   if (a.B > kWarpPlan) plan_run<C::THREADS>(a, 1, &bar.run, units, joins);
   tc_fence_before();
   __syncthreads();
@@ -174,11 +176,11 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
   const uint32_t tmem = bar.tmem_base;
 
   if (warp == kLoadK || warp == kLoadV) {
-    // ------------------------------------- producers: segments, Q and K; V
+    // ------------------------------------- producers: segments and K; Q and V
     // Both walk the run; the K warp hands its segments to the other roles.
     const bool is_k = warp == kLoadK;
     const OneTile tiles{};
-    const PlanRun<U> run = a.B > kWarpPlan ? bar.run : plan_warp<U>(a, 1, units, joins);
+    const PlanRun<U> run = a.B > kWarpPlan ? bar.run : plan_warp<U>(a, words, 1, units, joins);
     RunWalker<U, OneTile> walk(a, tiles, run, lane);
     const Segment& seg = walk.seg;
     TileRing<D> ring{is_k ? &tm_k : &tm_v, smem + (is_k ? 0 : C::KST * C::TILE_BYTES), bar.full + (is_k ? 0 : C::KST),
@@ -189,6 +191,8 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     while (ok && walk.advance()) {
       if (is_k) {
         if (!(ok = seg_publish(bar.ring, rst, rph, seg, lane, abort_flag, ws, 300))) break;
+      } else {  // (Q beside V, which is needed last, and several ahead, so that a wait for room
+                // holds up no keys: draft tokens over 64 to 4096 keys 27.7 -> 24.9 us)
         if (!(ok = warp_wait(&bar.q_empty[qb], qph ^ 1, abort_flag, ws, 301))) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&bar.q_full[qb], q_bytes);
@@ -196,7 +200,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
             tma_load_3d(sQ + qb * C::Q_BYTES + c * C::Q_CHUNK, &tm_q, &bar.q_full[qb], c * 64, seg.head * G, seg.start);
         }
         ++q_used;
-        if ((qb ^= 1) == 0) qph ^= 1;
+        if (++qb == C::QST) { qb = 0; qph ^= 1; }
       }
       for (int j = seg.j0; ok && j < seg.j1; ++j) {
         ok = ring.load(walk, j, lane, abort_flag, ws, is_k ? 302 : 304);
@@ -207,8 +211,8 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
     if (!ok) {
       ring.settle();
       int never = 0;
-      for (uint32_t s = 0; s < 2 && s < q_used; ++s)
-        mbar_wait(&bar.q_full[(q_used - 1 - s) & 1], ((q_used - 1 - s) >> 1) & 1, &never, nullptr, 0);
+      for (uint32_t s = 0; s < C::QST && s < q_used; ++s)
+        mbar_wait(&bar.q_full[(q_used - 1 - s) % C::QST], ((q_used - 1 - s) / C::QST) & 1, &never, nullptr, 0);
     }
   } else if (warp == kIssueS) {
     // ------------------------------------------------- S^T = K Q^T (128 x NR)
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(FewCfg<D, NR>::THREADS, 1)
           if ((sb ^= 1) == 0) sph ^= 1;
           if (++st == C::KST) { st = 0; ph ^= 1; }
         }
-        if ((qb ^= 1) == 0) qph ^= 1;
+        if (++qb == C::QST) { qb = 0; qph ^= 1; }
       }
       int never = 0;
       mma_commit(&bar.drain[0]);

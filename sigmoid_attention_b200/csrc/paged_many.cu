@@ -284,6 +284,8 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
   };
   // Single tiles where that is at most a.lone units per CTA, else pairs.
   auto settled = [&](U total) { return math.pairs || total <= static_cast<U>(a.lone) * gridDim.x; };
+  SeqWords words{};
+  if (a.B <= kWarpPlan && (warp == kLoadK || warp == kLoadV)) words = seq_load(a, lane);
   if (a.B > kWarpPlan) {
     for (;; math.pairs = 1) {
       plan_run<C::THREADS>(a, 1 << math.pairs, &bar.run, units, joins);
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
       run = bar.run;
     } else {
       for (;; math.pairs = 1) {
-        run = plan_warp<U>(a, 1 << math.pairs, units, joins);
+        run = plan_warp<U>(a, words, 1 << math.pairs, units, joins);
         if (settled(run.total)) break;
       }
     }

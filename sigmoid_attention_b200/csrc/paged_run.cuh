@@ -169,13 +169,13 @@ __device__ __forceinline__ void plan_run(const PagedAttend& a, int least, PlanRu
 // batch of 108 took 11.8 instead of 11.1 us).
 constexpr int kWarpPlan = 32;
 template <typename U, typename Units, typename Join>
-__device__ __forceinline__ PlanRun<U> plan_warp(const PagedAttend& a, int least, Units units, Join join) {
+__device__ __forceinline__ PlanRun<U> plan_warp(const PagedAttend& a, const SeqWords& words, int least, Units units, Join join) {
   const int lane = threadIdx.x & 31;
   PlanRun<U> run;
   SeqInfo s;
   U mine = 0;
   float longest = 0.f;
-  const bool good = seq_check(a, seq_load(a, lane), &s);
+  const bool good = seq_check(a, words, &s);
   if (lane < a.B) {
     if (!good) {
       if (blockIdx.x == 0) raise_invalid(a.ws, -(lane + 1));
