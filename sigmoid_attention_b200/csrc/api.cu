@@ -216,7 +216,9 @@ int check_paged_heads(int Hq, int Hkv, int d) {
 }
 
 // Whether a call's rows per key/value head are few enough for paged_few.cu.
-bool paged_is_few(int Hq, int Hkv, int max_q) { return static_cast<long long>(Hq / Hkv) * max_q <= kFewRows; }
+bool paged_is_few(int Hq, int Hkv, int d, int max_q) {
+  return static_cast<long long>(Hq / Hkv) * max_q <= few_rows(d);
+}
 
 // The workspace and device checks of a paged call.
 int check_paged_call(const void* ws, size_t ws_bytes, size_t need, DeviceInfo* info) {
@@ -676,7 +678,7 @@ int sigattn_paged_write(const void* k, long long k_stride, const void* v, long l
 
 size_t sigattn_paged_workspace_size(int Hq, int Hkv, int d, int max_seqlen_q) {
   if (check_paged_heads(Hq, Hkv, d) != SIGATTN_OK || max_seqlen_q < 1 || max_seqlen_q > kMaxPagedLen) return 0;
-  const size_t rows = paged_is_few(Hq, Hkv, max_seqlen_q) ? kFewRows : kFwdItemRows;
+  const size_t rows = paged_is_few(Hq, Hkv, d, max_seqlen_q) ? few_rows(d) : kFwdItemRows;
   return kHeaderBytes + 2 * kMaxPagedCtas * rows * d * sizeof(float);
 }
 
@@ -700,7 +702,7 @@ int sigattn_fwd_paged(const void* q, long long q_stride, const void* k_cache, co
   if (st != SIGATTN_OK || total == 0) return st;
   using bf16 = __nv_bfloat16;
   const int G = Hq / Hkv;
-  const bool few = paged_is_few(Hq, Hkv, max_seqlen_q);
+  const bool few = paged_is_few(Hq, Hkv, d, max_seqlen_q);
   // A bound on the call's units of work (paged_run.cuh).
   const int item = 2 * (128 / G);
   const double units = static_cast<double>(Hkv) * (max_pages * page_size / 128 + 1) * (few ? B : 2.0 * (total / item + B));

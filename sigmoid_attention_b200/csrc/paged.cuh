@@ -67,8 +67,12 @@ constexpr float kFewCut = 0.02f, kManyCut = 0.003f;
 // that a pair's better use of each key block wins: 1000 tokens over 30000 keys 162
 // / 141 us, and at d = 64 500 tokens over 10000 (16 units) 36 / 35, 30000 79 / 65.
 constexpr int kLoneUnits = 16;
-// Query rows per key/value head (G * new tokens) up to which paged_few.cu serves.
-constexpr int kFewRows = 64;
+// Query rows per key/value head (G * new tokens) up to which paged_few.cu serves;
+// beyond, paged_many.cu. Measured, few / many, 16 texts of 2000 keys, 8 heads: d = 64,
+// 32 rows 21.7 / 30.9 us, 50 28.9 / 31.7, 64 31.3 / 31.6; d = 128, 17 rows 30.3 / 32.6, 32
+// 33.5 / 32.1, 50 38.5 / 33.0, 64 43.5 / 33.0 (each thread's weights and the products'
+// columns grow with the rows).
+constexpr int few_rows(int d) { return d == 64 ? 64 : 32; }
 
 // One pair in one word (x1 low, x2 high) turned by (cos, sin) = cs.
 __device__ __forceinline__ uint32_t turn_word(uint32_t w, float2 cs) {

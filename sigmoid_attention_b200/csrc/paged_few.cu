@@ -1,6 +1,6 @@
 // paged_few.cu -- sigmoid attention of a few new tokens per sequence over a
-// paged cache (at most 64 query rows per key/value head: G query heads times
-// the new tokens).
+// paged cache (at most 64 query rows per key/value head, 32 at d = 128: G query
+// heads times the new tokens).
 //
 //   o_i = sum_{j < N} sigma(q_i . k_j / sqrt(d) - ln N) v_j
 //
@@ -60,7 +60,7 @@ struct FewCfg {
   // of its phases (a role that skipped one could take an earlier phase of the
   // same parity for the one it waits for). V tiles stay longer: they wait for P.
   static constexpr int KST = D == 64 ? 4 : 2;
-  static constexpr int VST = D == 64 ? 5 : (NR == 64 ? 2 : 3);
+  static constexpr int VST = D == 64 ? 5 : 3;
   static constexpr int STAGES = KST + VST;
   static constexpr int Q_CHUNK = NR * 128;
   static constexpr int Q_BYTES = CH * Q_CHUNK;
@@ -582,8 +582,7 @@ cudaError_t launch_few(int d, int rows, Args&&... args) {
     return launch_few_impl<64, 64, U>(args...);
   }
   if (rows <= 16) return launch_few_impl<128, 16, U>(args...);
-  if (rows <= 32) return launch_few_impl<128, 32, U>(args...);
-  return launch_few_impl<128, 64, U>(args...);
+  return launch_few_impl<128, 32, U>(args...);
 }
 
 }  // namespace
