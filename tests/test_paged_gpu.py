@@ -10,6 +10,7 @@ at most N 2^-24 A (twice that is allowed for); the output is rounded once
 (2^-8 |o|). So |got - o| <= (2^-8 + 1e-3 + N 2^-23) A + 2^-8 (|o| + the former).
 """
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -648,6 +649,36 @@ def test_attend_repeats_streams_and_graphs(q, kv):
         b.kv.copy_(i32(b.kv_lens))
     b.fine()
     b.fine(ws2)
+
+
+def test_attend_from_two_threads():
+    """Host threads with a stream and a workspace each (the calls release
+    Python's lock)."""
+    b = Batch([1, 90, 1], [3000, 400, 77], 8, 2, 64, 16)
+    want = b.run(True)
+    b.check(want, True)
+    torch.cuda.synchronize()
+    outs, errors = {}, []
+
+    def work(name):
+        try:
+            s, ws, o = torch.cuda.Stream(), torch.zeros_like(b.ws), torch.full_like(want, float("nan"))
+            torch.cuda.synchronize()
+            for _ in range(50):
+                b.run(True, o=o, ws=ws, stream=s)
+            s.synchronize()
+            outs[name] = (o, sa.sigattn_read_error(ws, s))
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not errors and len(outs) == 3
+    for o, status in outs.values():
+        assert status == (0, 0) and torch.equal(o, want)
 
 
 def test_attend_any_earlier_workspace_use():
