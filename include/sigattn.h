@@ -351,7 +351,10 @@ SIGATTN_API size_t sigattn_paged_workspace_size(int Hq, int Hkv, int d, int max_
  *  - max_seqlen_q >= every q_b (kernel choice, limits). kv_lens[b] <= max_pages
  *    * page_size. A sequence that breaks these rules, or whose cu_seqlens
  *    bounds are out of order or out of [0, total], gets no work: its rows are
- *    left untouched and the error word is raised (site -(b+1)).
+ *    left untouched and the error word is raised (site -(b+1)). So does one
+ *    whose rows start before the end of an earlier sequence that keeps these
+ *    rules (which takes bounds out of order between the two): no row belongs
+ *    to two sequences.
  *  - A page number outside [0, num_pages) among a sequence's pages contributes
  *    nothing to its sums and raises site 203. A batch of more than 2^31 key
  *    blocks (128 keys of one query tile) per SM gets no work and raises site 206.

@@ -44,7 +44,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 // (The lengths and tables below are loaded from L2: the kernel before this one
 // may write them while this one's CTAs are already resident.)
 // Sequence b's first row, new tokens m and cached tokens n; false (and m = 0)
-// if it breaks the call's rules.
+// if it breaks one of the rules that its own words show.
 struct SeqInfo {
   int start, m, n;
 };
@@ -56,13 +56,33 @@ __device__ __forceinline__ SeqWords seq_load(const PagedAttend& a, int b) {
   b = min(b, a.B - 1);
   return SeqWords{__ldcg(a.cu + b), __ldcg(a.cu + b + 1), __ldcg(a.kv + b)};
 }
+__device__ __forceinline__ bool seq_keeps(const SeqWords& w, int total, int max_q, int most) {
+  return w.start >= 0 && w.end >= w.start && w.end <= total && w.end - w.start <= max_q && w.n >= 0 && w.n <= most;
+}
 __device__ __forceinline__ bool seq_check(const PagedAttend& a, const SeqWords& w, SeqInfo* s) {
-  const bool ok = w.start >= 0 && w.end >= w.start && w.end <= a.total && w.end - w.start <= a.max_q && w.n >= 0 &&
-                  w.n <= a.max_pages << a.page_shift;
+  const bool ok = seq_keeps(w, a.total, a.max_q, a.max_pages << a.page_shift);
   s->start = w.start;
   s->m = ok ? w.end - w.start : 0;
   s->n = w.n;
   return ok;
+}
+
+// A further rule, that a sequence's rows start where or after those of all earlier
+// ones end: so no row has two sequences and the rows add up to at most `total`
+// (the host's bound on the units relies on it). Where every sequence passes
+// seq_check this holds by itself, since each starts where the one before ends; only
+// a batch with one that does not is looked through.
+// rows_before: where the rows of the sequences before b end that pass seq_check.
+static __device__ __noinline__ int rows_before(const int* cu, const int* kv, int b, int total, int max_q, int most) {
+  int reach = 0;
+  for (int i = 0; i < b; ++i) {
+    const SeqWords w{__ldcg(cu + i), __ldcg(cu + i + 1), __ldcg(kv + i)};
+    if (w.end > w.start && seq_keeps(w, total, max_q, most)) reach = max(reach, w.end);
+  }
+  return reach;
+}
+__device__ __forceinline__ int rows_before(const PagedAttend& a, int b) {
+  return rows_before(a.cu, a.kv, b, a.total, a.max_q, a.max_pages << a.page_shift);
 }
 
 // A CTA's run: `count` units from unit blockIdx.x * per of the line on, which is
@@ -72,6 +92,7 @@ struct PlanRun {
   U rem;
   SeqInfo s;
   int b, count, per;
+  int reach;  // rows_before(b), or -1 where every sequence passes seq_check
   int pairs;  // (paged_many.cu)
   U total;
 };
@@ -106,22 +127,16 @@ __device__ __forceinline__ void plan_run(const PagedAttend& a, int least, PlanRu
   const int chunk = ceil_div(a.B, THREADS);
   const int b0 = min(a.B, tid * chunk), b1 = min(a.B, b0 + chunk);
   SeqInfo s;  // of the sequence that units_of saw last
+  bool good = true, ordered = true;
   auto units_of = [&](int b, bool report) -> U {
-    if (!seq_check(a, seq_load(a, b), &s)) {
+    const bool keeps = seq_check(a, seq_load(a, b), &s);
+    good &= keeps;
+    if (!keeps || (!ordered && s.m > 0 && s.start < rows_before(a, b))) {
       if (report && blockIdx.x == 0) raise_invalid(a.ws, -(b + 1));
       return 0;
     }
     return s.m > 0 ? units(s) * static_cast<U>(a.Hkv) : 0;
   };
-  U mine = 0;
-  float longest = 0.f;
-  for (int b = b0; b < b1; ++b) {
-    const U u = units_of(b, true);
-    mine += u;
-    if (u > 0) longest = fmaxf(longest, join(s));
-  }
-  // (nonnegative floats order like their bits)
-  const unsigned most = __reduce_max_sync(0xffffffffu, __float_as_uint(longest));
   auto scan = [&](U v) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -130,12 +145,25 @@ __device__ __forceinline__ void plan_run(const PagedAttend& a, int least, PlanRu
     }
     return v;
   };
-  const U incl = scan(mine);
-  if (lane == 31) {
-    sums[warp] = incl;
-    joins[warp] = most;
+  U mine, incl;
+  for (;; ordered = false) {
+    mine = 0;
+    float longest = 0.f;
+    for (int b = b0; b < b1; ++b) {
+      const U u = units_of(b, true);
+      mine += u;
+      if (u > 0) longest = fmaxf(longest, join(s));
+    }
+    // (nonnegative floats order like their bits)
+    const unsigned most = __reduce_max_sync(0xffffffffu, __float_as_uint(longest));
+    incl = scan(mine);
+    if (lane == 31) {
+      sums[warp] = incl;
+      joins[warp] = most;
+    }
+    // Once more with the further rule if some sequence is bad.
+    if (__syncthreads_or(!good && ordered) == 0) break;
   }
-  __syncthreads();
   const U upto = scan(lane < kWarps ? sums[lane] : 0);
   const U total = __shfl_sync(0xffffffffu, upto, kWarps - 1);
   const U before = __shfl_sync(0xffffffffu, upto, warp > 0 ? warp - 1 : 0);
@@ -158,6 +186,7 @@ __device__ __forceinline__ void plan_run(const PagedAttend& a, int least, PlanRu
       rem -= u;
     }
     run->b = b;
+    run->reach = ordered ? -1 : rows_before(a, b);
     run->rem = rem;
     run->s = s;
   }
@@ -175,7 +204,17 @@ __device__ __forceinline__ PlanRun<U> plan_warp(const PagedAttend& a, const SeqW
   SeqInfo s;
   U mine = 0;
   float longest = 0.f;
-  const bool good = seq_check(a, words, &s);
+  bool good = seq_check(a, words, &s);
+  const bool ordered = __all_sync(0xffffffffu, good);
+  int reach = -1;
+  if (__builtin_expect(!ordered, 0)) {  // (rows_before by the warp)
+    int upto = s.m > 0 ? s.start + s.m : 0;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) upto = max(upto, __shfl_up_sync(0xffffffffu, upto, o));
+    reach = max(0, __shfl_up_sync(0xffffffffu, upto, 1));
+    if (lane == 0) reach = 0;
+    good &= s.m == 0 || s.start >= reach;
+  }
   if (lane < a.B) {
     if (!good) {
       if (blockIdx.x == 0) raise_invalid(a.ws, -(lane + 1));
@@ -200,6 +239,7 @@ __device__ __forceinline__ PlanRun<U> plan_warp(const PagedAttend& a, const SeqW
   const U base = incl - mine;
   const unsigned who = __ballot_sync(0xffffffffu, first >= base && first - base < mine);
   run.b = who ? __ffs(who) - 1 : 0;
+  run.reach = __shfl_sync(0xffffffffu, reach, run.b);
   run.rem = first - __shfl_sync(0xffffffffu, base, run.b);
   run.s = SeqInfo{__shfl_sync(0xffffffffu, s.start, run.b), __shfl_sync(0xffffffffu, s.m, run.b),
                   __shfl_sync(0xffffffffu, s.n, run.b)};
@@ -293,7 +333,8 @@ struct RunWalker {
   const PagedAttend& a;
   const Tiles& tiles;
   const int lane, per, count;
-  int pos;  // where the current item ends, counted from the run's first unit
+  int reach;  // PlanRun::reach, for sequence seq_base
+  int pos;    // where the current item ends, counted from the run's first unit
   Segment seg;
   SeqInfo s, next_s;
   U rem;    // before the first segment: where the run starts in its sequence
@@ -310,7 +351,15 @@ struct RunWalker {
       const int from = b + 1 - seq_base;  // 1 .. 32
       SeqInfo x;
       seq_check(a, seq_cur, &x);
-      unsigned found = __ballot_sync(0xffffffffu, x.m > 0 && seq_base + lane < a.B);
+      bool works = x.m > 0 && seq_base + lane < a.B;
+      int upto = x.m > 0 ? x.start + x.m : 0;
+      if (__builtin_expect(reach >= 0, 0)) {  // a bad sequence somewhere: none may start before an earlier one's end
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) upto = max(upto, __shfl_up_sync(0xffffffffu, upto, o));
+        const int before = __shfl_up_sync(0xffffffffu, upto, 1);
+        works &= x.start >= (lane > 0 ? max(before, reach) : reach);
+      }
+      unsigned found = __ballot_sync(0xffffffffu, works);
       found = from < 32 ? found >> from << from : 0u;
       if (found) {
         const int l = __ffs(found) - 1;
@@ -322,6 +371,7 @@ struct RunWalker {
       }
       seq_base += 32;
       if (seq_base >= a.B) break;
+      if (__builtin_expect(reach >= 0, 0)) reach = max(reach, __shfl_sync(0xffffffffu, upto, 31));
       seq_cur = seq_ahead;
       seq_ahead = seq_load(a, seq_base + 32 + lane);
       b = seq_base - 1;
@@ -342,7 +392,7 @@ struct RunWalker {
   }
 
   __device__ __forceinline__ RunWalker(const PagedAttend& args, const Tiles& t, const PlanRun<U>& run, int ln)
-      : a(args), tiles(t), lane(ln), per(run.per), count(run.count), pos(0) {
+      : a(args), tiles(t), lane(ln), per(run.per), count(run.count), reach(run.reach), pos(0) {
     if (count <= 0) return;
     s = run.s;
     rem = run.rem;

@@ -805,3 +805,57 @@ def test_cache_survives_a_refused_release():
     cache.release(i32([1, 0]))
     cache.check()
     assert cache.lens.tolist() == [1, 0] and int(cache.free_count) == 5
+
+
+# ---------------------------------------------------------------------------
+# Rules that a batch breaks as a whole
+# ---------------------------------------------------------------------------
+def working(cu, total, max_q):
+    """The header's rule, one sequence after another (kv_lens are good here)."""
+    works, reach = [], 0
+    for start, end in zip(cu[:-1], cu[1:]):
+        keeps = 0 <= start <= end <= total and end - start <= max_q
+        works.append(keeps and start >= reach)
+        if keeps and end > start:
+            reach = max(reach, end)
+    return works
+
+
+@pytest.mark.parametrize("B", [5, 40, 700])
+@pytest.mark.parametrize("m", [2, 90])
+@pytest.mark.parametrize("bounds", ["alternating", "partly", "last"])
+def test_attend_overlapping_rows_get_no_work(bounds, m, B):
+    """Bounds out of order, between which other sequences' bounds are in order
+    but cover rows that an earlier one has: no row gets two sequences, and the
+    workspace serves the next call."""
+    b = Batch([m] * B, [m + 13 * i % 300 for i in range(B)], 4, 2, 64, 16, seed=m + B)
+    good = b.run(True, ws=torch.zeros_like(b.ws))
+    cu, total = b.cu.tolist(), m * B
+    if bounds == "alternating":
+        cu = [m * (i % 2) for i in range(B + 1)]
+    elif bounds == "partly":
+        cu[2], cu[3] = m // 2, m // 2 + m  # sequence 1 is out of order, 2 has half of 0's rows, 3 follows it
+    else:
+        cu[B - 1] = total - 2 * m - 1  # the last but one is out of order, the last starts one row too early
+    max_q = 2 * m + 1
+    b.ws = workspace(sa.sigattn_paged_workspace_size(4, 2, 64, max_q))
+    kept, b.cu = b.cu, i32(cu)
+    works = working(cu, total, max_q)
+    assert False in works and True in works
+    o = b.run(True, max_q=max_q)
+    status, site = sa.sigattn_read_error(b.ws)
+    assert status == 1 and site < 0 and not works[-site - 1]
+    untouched = torch.ones(total, dtype=torch.bool, device=DEV)
+    for s in [s for s in range(B) if works[s] and cu[s + 1] > cu[s]]:
+        at, n = cu[s], cu[s + 1] - cu[s]
+        untouched[at:at + n] = False
+        if s < 8 or s > B - 4:
+            b.q_lens[s] = n
+            ref, A = b.exact(s, True)
+            inner = (2.0 ** -8 + 1e-3 + b.kv_lens[s] * 2.0 ** -23) * A
+            assert bool(((o[at:at + n].double() - ref).abs() <= inner + 2.0 ** -8 * (ref.abs() + inner)).all()), s
+    assert bool(o[untouched].isnan().all()) and not bool(o[~untouched].isnan().any())
+    b.cu = kept
+    assert torch.equal(b.run(True, max_q=max_q), b.run(True, max_q=max_q, ws=torch.zeros_like(b.ws)))
+    assert bool((b.run(True, max_q=max_q).float() - good.float()).abs().max() < 0.1)
+    b.fine()
