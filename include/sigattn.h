@@ -441,7 +441,9 @@ SIGATTN_API int sigattn_eval_sigmoid(const float* scores, float* p, float* slope
 
 /* Synchronise `stream`, read the workspace's sticky error word, clear it and
  * return it (SIGATTN_OK if no kernel reported a problem). If `site` is not
- * NULL it receives a code naming the failing check or wait (0 if none). */
+ * NULL it receives a code naming the failing check or wait (0 if none). Of
+ * several errors the first is kept, but SIGATTN_ERR_TIMEOUT replaces any
+ * other; after one the whole 256-byte header is cleared. */
 SIGATTN_API int sigattn_read_error(void* workspace, int* site, void* stream);
 
 #ifdef __cplusplus

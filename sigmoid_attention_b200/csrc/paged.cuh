@@ -88,10 +88,4 @@ __device__ __forceinline__ void turn_words(uint32_t& x, uint32_t& y, float2 lo, 
   y = pack_bf16x2(x2 * lo.x + x1 * lo.y, z2 * hi.x + z1 * hi.y);
 }
 
-// Raise SIGATTN_ERR_INVALID_ARG with `site` in the workspace header.
-__device__ __forceinline__ void raise_invalid(int* ws, int site) {
-  atomicCAS(ws + kHdrError, 0, 1 /* SIGATTN_ERR_INVALID_ARG */);
-  atomicExch(ws + kHdrErrorSite, site);
-}
-
 }  // namespace sigattn

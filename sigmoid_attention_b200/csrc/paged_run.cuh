@@ -92,9 +92,9 @@ struct PlanRun {
   U rem;
   SeqInfo s;
   int b, count, per;
-  int reach;  // rows_before(b), or -1 where every sequence passes seq_check
   int pairs;  // (paged_many.cu)
   U total;
+  int reach;  // rows_before(b), or -1 where every sequence passes seq_check
 };
 
 // How long the runs are: an equal share, at least `least` units, and by what the

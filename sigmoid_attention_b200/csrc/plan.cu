@@ -73,10 +73,7 @@ __global__ void __launch_bounds__(1024) prep_kernel(const int* __restrict__ leng
       n = __ldg(lengths + b);
       bad = n < 0 || n > L;
     }
-    if (bad) {
-      atomicCAS(err + kHdrError, 0, 1 /* SIGATTN_ERR_INVALID_ARG */);
-      atomicExch(err + kHdrErrorSite, -(b + 1));
-    }
+    if (bad) raise_invalid(err, -(b + 1));
     s_len[b] = bad ? 0 : n;
     s_start[b] = bad ? 0 : start;
     s_key[b] = work_rows(kind, s_len[b], kr) > 0 ? work_cols(kind, s_len[b], kr) : 0;

@@ -39,6 +39,21 @@ __device__ __forceinline__ unsigned long long globaltimer_ns() {
   return t;
 }
 
+// The error word and its site are one 64-bit word, so that both are always of one
+// error. raise_invalid: SIGATTN_ERR_INVALID_ARG, unless an error is there already.
+// raise_timeout: SIGATTN_ERR_TIMEOUT, which replaces any other, since counters may
+// have been left behind (sigattn_read_error then clears the whole header).
+static_assert(kHdrError == 0 && kHdrErrorSite == 1, "one aligned 64-bit word");
+__device__ __forceinline__ unsigned long long error_word(int code, int site) {
+  return static_cast<unsigned long long>(static_cast<uint32_t>(site)) << 32 | static_cast<uint32_t>(code);
+}
+__device__ __forceinline__ void raise_invalid(int* ws, int site) {
+  atomicCAS(reinterpret_cast<unsigned long long*>(ws), 0ull, error_word(1 /* SIGATTN_ERR_INVALID_ARG */, site));
+}
+__device__ __forceinline__ void raise_timeout(int* ws, int site) {
+  atomicExch(reinterpret_cast<unsigned long long*>(ws), error_word(4 /* SIGATTN_ERR_TIMEOUT */, site));
+}
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -103,10 +118,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
       if (*abort_flag) return false;
       if (globaltimer_ns() - t0 > limit_ns) {
         *abort_flag = 1;
-        if (ws_header != nullptr) {
-          atomicCAS(ws_header + kHdrError, 0, 4 /* SIGATTN_ERR_TIMEOUT */);
-          atomicExch(ws_header + kHdrErrorSite, site);
-        }
+        if (ws_header != nullptr) raise_timeout(ws_header, site);
         return false;
       }
     }

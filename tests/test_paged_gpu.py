@@ -859,3 +859,57 @@ def test_attend_overlapping_rows_get_no_work(bounds, m, B):
     assert torch.equal(b.run(True, max_q=max_q), b.run(True, max_q=max_q, ws=torch.zeros_like(b.ws)))
     assert bool((b.run(True, max_q=max_q).float() - good.float()).abs().max() < 0.1)
     b.fine()
+
+
+# ---------------------------------------------------------------------------
+# The sticky error word
+# ---------------------------------------------------------------------------
+def raise_no_pages(ws):
+    """SIGATTN_ERR_INVALID_ARG with site 202: one page wanted, none free."""
+    one, slots = i32([1]), i32([0])
+    sa.sigattn_paged_reserve(i32([0]), one, i32([[0]]), i32([0]), i32([0]), i32([0]), i32([0, 0]), i32([0]), slots, None, 16, ws)
+
+
+def raise_bad_slot(ws):
+    """SIGATTN_ERR_INVALID_ARG with site 204."""
+    k, cache = (torch.zeros(*s, dtype=torch.bfloat16, device=DEV) for s in ((1, 1, 64), (1, 1, 16, 64)))
+    sa.sigattn_paged_write(k, k, i32([99]), cache, cache.clone(), ws)
+
+
+def raise_bad_length(ws):
+    """SIGATTN_ERR_INVALID_ARG with site -1, by a whole-sequence call."""
+    x = torch.zeros(1, 1, 64, 64, dtype=torch.bfloat16, device=DEV)
+    sa.sigattn_fwd(x, x, x, torch.empty_like(x), i32([65]), ws)
+
+
+MILD = {"pages": (raise_no_pages, (1, 202)), "slot": (raise_bad_slot, (1, 204)), "length": (raise_bad_length, (1, -1))}
+
+
+@pytest.mark.parametrize("mild", MILD)
+def test_expired_wait_shows_beside_an_earlier_error(mild):
+    """An expired wait (here the diagnostic's, which must expire) may leave counts
+    in the header: it is reported, and the whole header cleared, whatever was
+    raised before or after it."""
+    fails, what = MILD[mild]
+    for first in (True, False):
+        ws = workspace(1024)
+        if first:
+            fails(ws)
+        ws.view(torch.int32)[5:46] = 3  # as if left behind by a call that gave up
+        sa.sigattn_selftest_wait_timeout(ws, limit_us=20000)
+        if not first:
+            fails(ws)
+        assert sa.sigattn_read_error(ws) == (4, 901)
+        assert not bool(ws.view(torch.int32)[:64].any())
+        fails(ws)
+        assert sa.sigattn_read_error(ws) == what
+
+
+@pytest.mark.parametrize("second", MILD)
+@pytest.mark.parametrize("first", MILD)
+def test_error_word_and_site_are_one_error(first, second):
+    """The first of several errors of one kind stays, with its own site."""
+    ws = workspace(1024)
+    for name in (first, second):
+        MILD[name][0](ws)
+    assert sa.sigattn_read_error(ws) == MILD[first][1]
