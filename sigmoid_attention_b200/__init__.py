@@ -578,8 +578,15 @@ class PagedCache:
         tokens, new_lens[b] (at most ``max_new``) of sequence b, in batch
         order; rows past them are ignored (their output rows are zero). With
         inv_freq, q and k are turned first, by ``positions`` or by each
-        token's place in its sequence. Returns [rows, Hq, d]."""
+        token's place in its sequence. Returns [rows, Hq, d]. If new_lens
+        breaks a bound or there are too few free pages, the cache stays as it
+        was, the rows are zero and the error word is raised."""
         rows = q.shape[0]
+        if rows > self.max_new:
+            # Attention would refuse such a sequence when its tokens are stored
+            # already; a length that reserve refuses stops the whole step.
+            # (With fewer rows reserve's own bound on them covers this.)
+            new_lens = torch.where(new_lens > self.max_new, -1, new_lens)
         slots = torch.empty(rows, dtype=torch.int32, device=q.device)
         places = torch.empty_like(slots)
         sigattn_paged_reserve(self.lens, new_lens, self.block_table, self.free_pages, self.free_count, self.free_count,

@@ -913,3 +913,46 @@ def test_error_word_and_site_are_one_error(first, second):
     for name in (first, second):
         MILD[name][0](ws)
     assert sa.sigattn_read_error(ws) == MILD[first][1]
+
+
+# ---------------------------------------------------------------------------
+# PagedCache: a call is met whole or changes nothing
+# ---------------------------------------------------------------------------
+def caches(n, Hq=4, Hkv=2, d=64, pages=12, max_new=4):
+    """n equal caches of two sequences of 7 and 18 tokens, and a source of rows."""
+    g = torch.Generator(device=DEV).manual_seed(11)
+    normal = lambda rows, h: torch.randn(rows, h, d, generator=g, device=DEV).to(torch.bfloat16)  # noqa: E731
+    rows = lambda m: (normal(m, Hq), normal(m, Hkv), normal(m, Hkv))  # noqa: E731
+    made = [sa.PagedCache(pages, 16, Hq, Hkv, d, 2, 6, max_new=max_new) for _ in range(n)]
+    for new in ([4, 4], [3, 4], [0, 4], [0, 4], [0, 2]):
+        x = rows(sum(new))
+        for c in made:
+            c.step(*x, i32(new))
+    for c in made:
+        c.check()
+    return made, rows
+
+
+def state(c):
+    held = [c.block_table[b, :ceil(n, c.page_size)].tolist() for b, n in enumerate(c.lens.tolist())]
+    return c.lens.tolist(), held, c.free_pages[:int(c.free_count)].tolist()
+
+
+def goes_on_like(c, other, rows):
+    """Both caches answer the next steps with the same bits."""
+    for new in ([1, 1], [4, 0], [2, 3]):
+        x = rows(sum(new))
+        assert torch.equal(c.step(*x, i32(new)), other.step(*x, i32(new)))
+    c.check()
+    assert state(c) == state(other)
+
+
+@pytest.mark.parametrize("new, rows, site", [([5, 1], 6, -1), ([1, 40], 41, -2), ([1, 5], 9, -2), ([4, 1], 4, 201)])
+def test_step_over_its_bound_changes_nothing(new, rows, site):
+    (c, other), make = caches(2)
+    before = state(c)
+    o = c.step(*make(rows), i32(new))
+    with pytest.raises(sa.SigattnError, match=str(site)):
+        c.check()
+    assert bool((o == 0).all()) and state(c) == before
+    goes_on_like(c, other, make)
