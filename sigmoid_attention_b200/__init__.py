@@ -591,18 +591,30 @@ class PagedCache:
         places = torch.empty_like(slots)
         sigattn_paged_reserve(self.lens, new_lens, self.block_table, self.free_pages, self.free_count, self.free_count,
                               self.cu_seqlens, self.lens, slots, places, self.page_size, self.workspace)
-        if inv_freq is None:
-            sigattn_paged_write(k, v, slots, self.k, self.v, self.workspace)
-        else:
-            turned = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            sigattn_paged_write(k, v, slots, self.k, self.v, self.workspace, q=q, q_out=turned,
-                                positions=places if positions is None else positions, inv_freq=inv_freq,
-                                pair_axis=pair_axis, adjacent=adjacent)
-            q = turned
-        o = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
-        sigattn_fwd_paged(q, self.k, self.v, o, self.cu_seqlens, self.lens, self.block_table, self.max_new, causal,
-                          self.workspace)
+        try:
+            if inv_freq is None:
+                sigattn_paged_write(k, v, slots, self.k, self.v, self.workspace)
+            else:
+                turned = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                sigattn_paged_write(k, v, slots, self.k, self.v, self.workspace, q=q, q_out=turned,
+                                    positions=places if positions is None else positions, inv_freq=inv_freq,
+                                    pair_axis=pair_axis, adjacent=adjacent)
+                q = turned
+            o = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+            sigattn_fwd_paged(q, self.k, self.v, o, self.cu_seqlens, self.lens, self.block_table, self.max_new, causal,
+                              self.workspace)
+        except Exception:
+            self._take_back()
+            raise
         return o
+
+    def _take_back(self) -> None:
+        """Undo the last reserve (none of its sequences, if the device refused
+        it): the pages that it popped still stand above the stack's height."""
+        before = self.lens - self.cu_seqlens.diff()
+        pages = lambda n: (n + self.page_size - 1) // self.page_size  # noqa: E731
+        self.free_count += (pages(self.lens) - pages(before)).sum(dtype=torch.int32)
+        self.lens.copy_(before)
 
     def release(self, keep_lens=None) -> None:
         """Keep the first keep_lens[b] tokens of every sequence (None: none)

@@ -956,3 +956,35 @@ def test_step_over_its_bound_changes_nothing(new, rows, site):
         c.check()
     assert bool((o == 0).all()) and state(c) == before
     goes_on_like(c, other, make)
+
+
+def test_step_with_refused_arguments_changes_nothing():
+    """Arguments that a later call of the step refuses, after pages were taken."""
+    (c, other), make = caches(2)
+    before, stack = state(c), c.free_pages.tolist()
+    q, k, v = make(5)
+    wide = torch.cat([q] * 16, 1)  # more heads than the workspace was made for
+    freq = torch.ones(8, device=DEV)
+    for bad in (dict(k=k[:, :1]), dict(v=v[:3]), dict(v=v.float()), dict(q=q[..., :32]), dict(q=q[:, :3]), dict(q=wide),
+                dict(q=q.float()), dict(inv_freq=freq[:3]), dict(inv_freq=freq.double()),
+                dict(inv_freq=freq, positions=i32([1])), dict(inv_freq=freq, pair_axis=i32([0])),
+                dict(k=k.cpu()), dict(q=q.transpose(1, 2))):
+        a = {**dict(q=q, k=k, v=v), **bad}
+        with pytest.raises((ValueError, sa.SigattnError)):
+            c.step(a.pop("q"), a.pop("k"), a.pop("v"), i32([1, 3]), **a)
+        assert state(c) == before and c.free_pages.tolist() == stack, bad
+    c.check()
+    goes_on_like(c, other, make)
+
+
+def test_refused_arguments_of_a_refused_step():
+    """Both at once: reserve refuses the lengths, a later call the arguments."""
+    (c, other), make = caches(2)
+    before = state(c)
+    q, k, v = make(4)
+    with pytest.raises(ValueError):
+        c.step(q, k[:, :1], v, i32([1, 200]))
+    with pytest.raises(sa.SigattnError):
+        c.check()
+    assert state(c) == before
+    goes_on_like(c, other, make)
