@@ -612,21 +612,27 @@ class PagedCache:
         """Undo the last reserve (none of its sequences, if the device refused
         it): the pages that it popped still stand above the stack's height."""
         before = self.lens - self.cu_seqlens.diff()
-        pages = lambda n: (n + self.page_size - 1) // self.page_size  # noqa: E731
-        self.free_count += (pages(self.lens) - pages(before)).sum(dtype=torch.int32)
+        self.free_count += (self._pages(self.lens) - self._pages(before)).sum(dtype=torch.int32)
         self.lens.copy_(before)
+
+    def _pages(self, lens):
+        return (lens + self.page_size - 1) // self.page_size
 
     def release(self, keep_lens=None) -> None:
         """Keep the first keep_lens[b] tokens of every sequence (None: none)
-        and give the other pages back. If a sequence holds fewer than that,
-        nothing changes and the error word is raised."""
+        and give the other pages back. If a sequence holds fewer than that, or
+        the stack has no room for the pages, nothing changes and the error word
+        is raised."""
+        height = self.free_count.clone()
         sigattn_paged_release(self.lens, keep_lens, self.block_table, self.free_pages, self.free_count, self.free_count,
                               self.page_size, self.workspace)
-        if keep_lens is None:
-            self.lens.zero_()
-        else:
-            met = ((keep_lens >= 0) & (keep_lens <= self.lens)).all()
-            self.lens.copy_(torch.where(met, keep_lens, self.lens))
+        # The lengths follow where the call was met: its rules once more.
+        keep = torch.zeros_like(self.lens) if keep_lens is None else keep_lens.reshape(self.lens.shape)
+        given = (self._pages(self.lens) - self._pages(keep)).sum()
+        most = self.block_table.shape[1] * self.page_size
+        met = ((keep >= 0) & (keep <= self.lens) & (self.lens <= most)).all()
+        met &= (height >= 0).all() & (height + given <= self.free_pages.numel()).all()
+        self.lens.copy_(torch.where(met, keep, self.lens))
 
     def check(self) -> None:
         """Synchronise and raise if a call reported a problem on the device."""

@@ -988,3 +988,38 @@ def test_refused_arguments_of_a_refused_step():
         c.check()
     assert state(c) == before
     goes_on_like(c, other, make)
+
+
+@pytest.mark.parametrize("keep, count, met", [
+    (None, 1, False), ([0, 0], 1, False), ([1, 0], 1, True), ([7, 17], 1, True), ([0, 1], 1, True),
+    ([7, 17], 4, False), ([7, 17], -1, False), (None, 0, True),
+])
+def test_release_that_the_stack_refuses_changes_nothing(keep, count, met):
+    """More pages than the stack has room for (two sequences share a page of
+    three, another is free: one too many), or a height that cannot be: the
+    device pushes none, so the lengths stay."""
+    (c,), _ = caches(1, pages=3)
+    lens, pages = state(c)[:2]
+    assert lens == [7, 18]
+    if count == 1:
+        c.free_pages[0] = pages[1][0]
+        c.block_table[1, 0] = pages[0][0]
+    c.free_count.fill_(count)
+    c.release(None if keep is None else i32(keep))
+    if met:
+        c.check()
+        keep = keep or [0, 0]
+        assert c.lens.tolist() == keep
+        assert int(c.free_count) == count + sum(ceil(n, 16) - ceil(m, 16) for n, m in zip(lens, keep))
+    else:
+        with pytest.raises(sa.SigattnError, match="202"):
+            c.check()
+        assert c.lens.tolist() == lens and int(c.free_count) == count
+
+
+def test_release_takes_lengths_of_any_shape():
+    """As sigattn_paged_release does: B numbers."""
+    (c,), _ = caches(1, pages=3)
+    c.release(i32([[6], [3]]))
+    c.check()
+    assert c.lens.tolist() == [6, 3] and int(c.free_count) == 1
