@@ -1023,3 +1023,110 @@ def test_release_takes_lengths_of_any_shape():
     c.release(i32([[6], [3]]))
     c.check()
     assert c.lens.tolist() == [6, 3] and int(c.free_count) == 1
+
+
+# ---------------------------------------------------------------------------
+# Paths of large calls
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("T", [2369, 4737, 5000])
+@pytest.mark.parametrize("d, Hq, Hkv, pairs, axes, adjacent", [
+    (64, 4, 2, 32, 3, False), (128, 6, 1, 48, 3, True), (64, 1, 1, 16, 1, True), (128, 2, 2, 64, 2, False), (64, 3, 1, 0, 1, False),
+])
+def test_write_more_tokens_than_warps(d, Hq, Hkv, pairs, axes, adjacent, T):
+    """More than 16 tokens per SM: warps go from token to token, the next rows,
+    slots and positions loaded ahead; with queries turned in place as well."""
+    g = torch.Generator(device=DEV).manual_seed(d + T)
+    ps, num = 64, ceil(T, 64) + 3
+    qkv = torch.randn(T, Hq + 2 * Hkv, d, generator=g, device=DEV).to(torch.bfloat16)
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    slots = torch.randperm(num * ps, generator=g, device=DEV)[:T].to(torch.int32)
+    slots[torch.rand(T, generator=g, device=DEV) < 0.1] = -1
+    slots[-1] = -1
+    kc = torch.full((num, Hkv, ps, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    vc = torch.full_like(kc, -7.0)
+    want_k, want_v = kc.double(), vc.double()
+    extra = {}
+    if pairs:
+        extra = dict(positions=torch.randint(0, 1 << 20, (axes, T), generator=g, device=DEV, dtype=torch.int32),
+                     inv_freq=10000.0 ** (-torch.arange(pairs, device=DEV, dtype=torch.float32) / pairs),
+                     pair_axis=torch.randint(0, axes, (pairs,), generator=g, device=DEV, dtype=torch.int32))
+    turned = lambda x: turn_ref(x, *extra.values(), adjacent) if pairs else x.double()  # noqa: E731
+    rq, rk, before = turned(q), turned(k), q.clone()
+    q_out, ws = torch.full((T, Hq, d), float("nan"), dtype=torch.bfloat16, device=DEV), workspace()
+    sa.sigattn_paged_write(k, v, slots, kc, vc, ws, q=q, q_out=q_out, adjacent=adjacent, **extra)
+    close_turned(q_out, rq, q)
+    keep = slots >= 0
+    p, o = (slots[keep] // ps).long(), (slots[keep] % ps).long()
+    close_turned(kc[p, :, o], rk[keep], k[keep])
+    want_v[p, :, o] = v[keep].double()
+    want_k[p, :, o] = kc[p, :, o].double()
+    assert torch.equal(vc.double(), want_v) and torch.equal(kc.double(), want_k)
+    k2, v2 = torch.full_like(kc, 7.0), torch.full_like(vc, -7.0)
+    rest = qkv[:, Hq:].clone()
+    sa.sigattn_paged_write(k, v, slots, k2, v2, ws, q=q, q_out=q, adjacent=adjacent, **extra)
+    assert torch.equal(q, q_out) and torch.equal(qkv[:, Hq:], rest) and (not pairs or not torch.equal(q, before))
+    assert torch.equal(k2, kc) and torch.equal(v2, vc)
+    assert sa.sigattn_read_error(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("B, max_pages, ps", [(100, 11, 16), (257, 12, 32), (1024, 40, 16), (4096, 5, 64), (4096, 200, 16)])
+def test_release_large_batches(B, max_pages, ps):
+    """Calls of several CTAs, the height in place, several on one workspace."""
+    g = np.random.default_rng(B + max_pages)
+    kv = g.integers(0, max_pages * ps + 1, B)
+    kv[0], kv[-1] = max_pages * ps, 1
+    spare = 7
+    table, stack = page_state(kv.tolist(), ps, max_pages, spare, B)
+    t, s, f, ws = i32(table.tolist()), i32(stack.tolist()), i32([spare]), workspace()
+    want = stack[:spare].tolist()
+    for keep in (g.integers(0, kv + 1), None):
+        first = np.zeros_like(kv) if keep is None else keep
+        sa.sigattn_paged_release(i32(kv.tolist()), None if keep is None else i32(keep.tolist()), t, s, f, f, ps, ws)
+        for b in range(B):
+            want += table[b, ceil(int(first[b]), ps):ceil(int(kv[b]), ps)].tolist()
+        assert int(f) == len(want)
+        assert s[:len(want)].tolist() == want
+        kv = first
+    assert sorted(want) == list(range(len(stack)))
+    assert sa.sigattn_read_error(ws) == (0, 0) and not bool(ws.any())
+
+
+def test_single_token_steps_of_a_cache_for_single_tokens():
+    """PagedCache with max_new = 1 (few query rows per key/value head), steps
+    captured and replayed, against attention in 64 bits over what the cache
+    holds."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    B, Hq, Hkv, d, n = 40, 8, 2, 128, 150
+    cache = sa.PagedCache(B * 10, 16, Hq, Hkv, d, B, 10)
+    normal = lambda h: torch.randn(B, h, d, generator=g, device=DEV).to(torch.bfloat16)  # noqa: E731
+    freq = 100.0 ** (-torch.arange(32, device=DEV, dtype=torch.float32) / 32)
+    new = i32([1] * B)
+    sq, sk, sv = normal(Hq), normal(Hkv), normal(Hkv)
+    cache.step(sq, sk, sv, new, inv_freq=freq)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = cache.step(sq, sk, sv, new, inv_freq=freq)
+    for i in range(2, n + 1):
+        for dst, h in ((sq, Hq), (sk, Hkv), (sv, Hkv)):
+            dst.copy_(normal(h))
+        graph.replay()
+        if i not in (2, 16, 17, 128, 129, n):
+            continue
+        pos = torch.full((B,), i - 1, dtype=torch.int32, device=DEV)
+        rq = turn_ref(sq, pos, freq, None, False).to(torch.bfloat16).double().view(B, Hkv, Hq // Hkv, d)
+        rows = lambda c: c[cache.block_table[:, :ceil(i, 16)].long()].transpose(1, 2).reshape(B, Hkv, -1, d)[:, :, :i].double()  # noqa: E731
+        k, v = rows(cache.k), rows(cache.v)
+        close_turned(k[:, :, -1], turn_ref(sk, pos, freq, None, False), sk)
+        assert torch.equal(v[:, :, -1], sv.double())
+        w = torch.sigmoid(torch.einsum("bhgd,bhjd->bhgj", rq, k) / math.sqrt(d) - math.log(i))
+        ref = torch.einsum("bhgj,bhjd->bhgd", w, v).reshape(B, Hq, d)
+        A = torch.einsum("bhgj,bhjd->bhgd", w, v.abs()).reshape(B, Hq, d)
+        # (0.02 A: a turned query that rounds the other way, as in the test of whole prompts)
+        assert bool(((out.double() - ref).abs() <= 0.02 * A).all()), i
+    cache.check()
+    assert cache.lens.tolist() == [n] * B
+    new.fill_(2)  # over the bound: refused whole, in the graph as well
+    graph.replay()
+    with pytest.raises(sa.SigattnError):
+        cache.check()
+    assert cache.lens.tolist() == [n] * B and bool((out == 0).all())
