@@ -336,7 +336,8 @@ def _paged():
         try:
             from . import _binding as module
         except ImportError as e:
-            raise RuntimeError("_binding.so is missing: run `python -m sigmoid_attention_b200.build` first") from e
+            raise RuntimeError("_binding.so is missing, or built for another Python or torch: run "
+                               f"`python -m sigmoid_attention_b200.build` ({e})") from e
         _calls = module
     return _calls
 

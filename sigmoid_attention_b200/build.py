@@ -11,6 +11,9 @@ import concurrent.futures
 import os
 import shutil
 import subprocess
+import sys
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -31,55 +34,68 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _deps() -> list[str]:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".cpp"))]
-    return files + [os.path.join(ROOT, "include", "sigattn.h")]
+def _fresh(made: str, *suffixes: str) -> bool:
+    """Is `made` newer than the public header and the sources that end so?"""
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(suffixes)]
+    files.append(os.path.join(ROOT, "include", "sigattn.h"))
+    return os.path.exists(made) and os.path.getmtime(made) >= max(os.path.getmtime(f) for f in files)
+
+
+def _binding_stamp() -> str:
+    """What the binding is built for besides its source."""
+    return f"{sys.version}\ntorch {torch.__version__}\n"
+
+
+def _binding_fresh() -> bool:
+    stamp = os.path.join(BUILD, "binding.stamp")
+    if not os.path.exists(stamp):
+        return False
+    with open(stamp) as f:
+        return f.read() == _binding_stamp() and _fresh(BINDING, ".cpp")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and os.path.exists(LIB) and os.path.exists(BINDING):
-        newest = max(os.path.getmtime(f) for f in _deps())
-        if min(os.path.getmtime(LIB), os.path.getmtime(BINDING)) >= newest:
-            return LIB
+    """The C library, and after it (compiled beside it) the binding: if that
+    fails the library is there all the same."""
+    lib, binding = force or not _fresh(LIB, ".cu", ".cuh"), force or not _binding_fresh()
     os.makedirs(BUILD, exist_ok=True)
-    nvcc = _nvcc()
-
-    def compile_one(src: str) -> str:
-        obj = os.path.join(BUILD, src.replace(".cu", ".o"))
-        cmd = [nvcc, *ARCH, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
-        if verbose:
-            cmd.insert(1, "-Xptxas=-v")
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
-        if verbose:
-            print(r.stderr)
-        return obj
-
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
-        objs = list(ex.map(compile_one, SOURCES))
-        binding_obj = binding.result()
-    tmp = LIB + ".tmp"
-    r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+        obj = ex.submit(_compile_binding) if binding else None
+        if lib:
+            _link_library(list(ex.map(lambda src: _compile_cuda(src, verbose), SOURCES)))
+        if binding:
+            _link_binding(obj.result())
     return LIB
 
 
-def _run(what: str, cmd: list[str]) -> None:
+def _compile_cuda(src: str, verbose: bool) -> str:
+    obj = os.path.join(BUILD, src.replace(".cu", ".o"))
+    cmd = [_nvcc(), *ARCH, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+    if verbose:
+        cmd.insert(1, "-Xptxas=-v")
+    out = _run(f"nvcc for {src}", cmd)
+    if verbose:
+        print(out)
+    return obj
+
+
+def _link_library(objs: list[str]) -> None:
+    tmp = LIB + ".tmp"
+    _run("link of libsigattn.so", [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs])
+    os.replace(tmp, LIB)
+
+
+def _run(what: str, cmd: list[str]) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r.stderr
 
 
 def _compile_binding() -> str:
     """csrc/binding.cpp against this Python's and torch's headers."""
     import sysconfig
 
-    import torch
     from torch.utils import cpp_extension
 
     obj = os.path.join(BUILD, "binding.o")
@@ -99,9 +115,9 @@ def _link_binding(obj: str) -> None:
         "g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libsigattn.so", "-Wl,-rpath,$ORIGIN",
         *[x for d in cpp_extension.library_paths() for x in ("-L", d)], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
     os.replace(tmp, BINDING)
+    with open(os.path.join(BUILD, "binding.stamp"), "w") as f:
+        f.write(_binding_stamp())
 
 
 if __name__ == "__main__":
-    import sys
-
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
