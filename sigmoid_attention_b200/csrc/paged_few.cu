@@ -83,17 +83,6 @@ struct FewCfg {
   static constexpr int THREADS = (kIssueO + 2) * 32;
 };
 
-// All new tokens of a sequence make one tile.
-struct OneTile {
-  __device__ __forceinline__ int items(const SeqInfo&) const { return 1; }
-  __device__ __forceinline__ int blocks(const SeqInfo& s, int) const { return seq_blocks(s.n); }
-  __device__ __forceinline__ int shift(const SeqInfo&, int) const { return 0; }
-  template <typename U>
-  __device__ __forceinline__ U before(const SeqInfo& s, int k) const {
-    return static_cast<U>(k) * seq_blocks(s.n);
-  }
-};
-
 template <int STAGES, int QST, typename U>
 struct FewBarriers {
   uint64_t full[STAGES], empty[STAGES];  // K slots first, then V slots

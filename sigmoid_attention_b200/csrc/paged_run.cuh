@@ -17,14 +17,9 @@
 #include <climits>
 
 #include "paged.cuh"
+#include "paged_tiles.cuh"
 
 namespace sigattn {
-
-constexpr int kKeyBlock = 128;
-
-// Key blocks that a tile seeing n keys walks (one even without keys: its rows
-// are written as zeros).
-__device__ __forceinline__ int seq_blocks(int n) { return n > 0 ? (n + kKeyBlock - 1) / kKeyBlock : 1; }
 
 // mbar_wait with its slow path out of line: inlined at every wait, the clock and
 // abort code made the roles' loops too long for the instruction cache.
@@ -43,12 +38,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 
 // (The lengths and tables below are loaded from L2: the kernel before this one
 // may write them while this one's CTAs are already resident.)
-// Sequence b's first row, new tokens m and cached tokens n; false (and m = 0)
-// if it breaks one of the rules that its own words show.
-struct SeqInfo {
-  int start, m, n;
-};
-// (as loaded: loads are issued ahead and checked when they are needed)
+// Sequence b's words as loaded: loads are issued ahead and checked when they are
+// needed.
 struct SeqWords {
   int start, end, n;
 };
@@ -59,6 +50,7 @@ __device__ __forceinline__ SeqWords seq_load(const PagedAttend& a, int b) {
 __device__ __forceinline__ bool seq_keeps(const SeqWords& w, int total, int max_q, int most) {
   return w.start >= 0 && w.end >= w.start && w.end <= total && w.end - w.start <= max_q && w.n >= 0 && w.n <= most;
 }
+// False (and m = 0) if the sequence breaks one of the rules that its own words show.
 __device__ __forceinline__ bool seq_check(const PagedAttend& a, const SeqWords& w, SeqInfo* s) {
   const bool ok = seq_keeps(w, a.total, a.max_q, a.max_pages << a.page_shift);
   s->start = w.start;
