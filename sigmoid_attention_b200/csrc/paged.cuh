@@ -1,4 +1,5 @@
-// paged.cuh -- arguments of the paged-cache kernels (pages.cu, paged.cu).
+// paged.cuh -- arguments of the paged-cache kernels (pages.cu, paged_few.cu,
+// paged_many.cu).
 #pragma once
 
 #include "common.cuh"
