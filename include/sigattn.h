@@ -290,6 +290,16 @@ SIGATTN_API int sigattn_paged_reserve(const int32_t* cached_lens, const int32_t*
                                       int32_t* cu_seqlens, int32_t* kv_lens, int32_t* slots, int32_t* positions, int B,
                                       int max_pages, int page_size, int num_pages, int rows, void* workspace,
                                       size_t workspace_bytes, void* stream);
+/* The same with a bound on the new tokens of one sequence: more than max_new
+ * (>= 0) are refused like any other bad length. With the max_seqlen_q of the
+ * sigattn_fwd_paged call that follows, a step that this call would refuse in
+ * part is refused whole, before its tokens are stored. */
+SIGATTN_API int sigattn_paged_reserve_bounded(const int32_t* cached_lens, const int32_t* new_lens,
+                                              int32_t* block_table, const int32_t* free_pages,
+                                              const int32_t* free_count, int32_t* free_count_out, int32_t* cu_seqlens,
+                                              int32_t* kv_lens, int32_t* slots, int32_t* positions, int B,
+                                              int max_pages, int page_size, int num_pages, int rows, int max_new,
+                                              void* workspace, size_t workspace_bytes, void* stream);
 
 /* Give pages back: sequence b holds kv_lens[b] tokens and keeps the first
  * keep_lens[b] (keep_lens NULL: none). Its pages [ceil(keep / page_size),
@@ -304,6 +314,14 @@ SIGATTN_API int sigattn_paged_release(const int32_t* kv_lens, const int32_t* kee
                                       int32_t* free_pages, const int32_t* free_count, int32_t* free_count_out, int B,
                                       int max_pages, int page_size, int num_pages, void* workspace,
                                       size_t workspace_bytes, void* stream);
+/* The same, and what the sequences hold afterwards goes to kv_lens_out (int32
+ * [B], may be kv_lens itself): keep_lens (or zeros) if the call was met, else
+ * kv_lens. */
+SIGATTN_API int sigattn_paged_release_lens(const int32_t* kv_lens, const int32_t* keep_lens,
+                                           const int32_t* block_table, int32_t* free_pages,
+                                           const int32_t* free_count, int32_t* free_count_out, int32_t* kv_lens_out,
+                                           int B, int max_pages, int page_size, int num_pages, void* workspace,
+                                           size_t workspace_bytes, void* stream);
 
 /* Store new keys and values in their slots and, with rotary positions, turn
  * the keys (and queries) on the way. k, v: `rows` rows of [Hkv][d]; row t goes to

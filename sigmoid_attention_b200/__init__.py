@@ -109,8 +109,12 @@ def library():
         lib.sigattn_softmax_fwd.argtypes = [_vp] * 5 + [_i] * 4 + [_vp, _sz, _vp]
         lib.sigattn_paged_reserve.restype = _i
         lib.sigattn_paged_reserve.argtypes = [_vp] * 10 + [_i] * 5 + [_vp, _sz, _vp]
+        lib.sigattn_paged_reserve_bounded.restype = _i
+        lib.sigattn_paged_reserve_bounded.argtypes = [_vp] * 10 + [_i] * 6 + [_vp, _sz, _vp]
         lib.sigattn_paged_release.restype = _i
         lib.sigattn_paged_release.argtypes = [_vp] * 6 + [_i] * 4 + [_vp, _sz, _vp]
+        lib.sigattn_paged_release_lens.restype = _i
+        lib.sigattn_paged_release_lens.argtypes = [_vp] * 7 + [_i] * 4 + [_vp, _sz, _vp]
         lib.sigattn_paged_write.restype = _i
         lib.sigattn_paged_write.argtypes = [_vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp, _ll, _vp, _ll, _vp, _vp, _vp] + [
             _i] * 9 + [_vp, _sz, _vp]
@@ -347,22 +351,25 @@ def _handle(stream):
 
 
 def sigattn_paged_reserve(cached_lens, new_lens, block_table, free_pages, free_count, free_count_out, cu_seqlens,
-                          kv_lens, slots, positions, page_size: int, workspace, stream=None) -> None:
-    """Take pages for new_lens[b] more tokens of every sequence and write
-    cu_seqlens, kv_lens, slots and positions (None to omit) for them."""
+                          kv_lens, slots, positions, page_size: int, workspace, stream=None, max_new=None) -> None:
+    """Take pages for new_lens[b] (at most max_new) more tokens of every
+    sequence and write cu_seqlens, kv_lens, slots and positions (None to omit)
+    for them."""
     st = (_calls or _paged()).paged_reserve(
         cached_lens, new_lens, block_table, free_pages, free_count, free_count_out, cu_seqlens, kv_lens, slots, positions,
-        page_size, workspace, _handle(stream))
+        page_size, workspace, max_new, _handle(stream))
     if st:
         _check("sigattn_paged_reserve", st)
 
 
 def sigattn_paged_release(kv_lens, keep_lens, block_table, free_pages, free_count, free_count_out, page_size: int,
-                          workspace, stream=None) -> None:
+                          workspace, stream=None, kv_lens_out=None) -> None:
     """Push the pages past each sequence's first keep_lens[b] tokens (None: all
-    pages) back on the stack of free pages."""
+    pages) back on the stack of free pages; what the sequences then hold goes
+    to kv_lens_out (kv_lens itself, or None to omit)."""
     st = (_calls or _paged()).paged_release(
-        kv_lens, keep_lens, block_table, free_pages, free_count, free_count_out, page_size, workspace, _handle(stream))
+        kv_lens, keep_lens, block_table, free_pages, free_count, free_count_out, page_size, workspace, kv_lens_out,
+        _handle(stream))
     if st:
         _check("sigattn_paged_release", st)
 
@@ -583,15 +590,11 @@ class PagedCache:
         breaks a bound or there are too few free pages, the cache stays as it
         was, the rows are zero and the error word is raised."""
         rows = q.shape[0]
-        if rows > self.max_new:
-            # Attention would refuse such a sequence when its tokens are stored
-            # already; a length that reserve refuses stops the whole step.
-            # (With fewer rows reserve's own bound on them covers this.)
-            new_lens = torch.where(new_lens > self.max_new, -1, new_lens)
         slots = torch.empty(rows, dtype=torch.int32, device=q.device)
         places = torch.empty_like(slots)
         sigattn_paged_reserve(self.lens, new_lens, self.block_table, self.free_pages, self.free_count, self.free_count,
-                              self.cu_seqlens, self.lens, slots, places, self.page_size, self.workspace)
+                              self.cu_seqlens, self.lens, slots, places, self.page_size, self.workspace,
+                              max_new=self.max_new)
         try:
             if inv_freq is None:
                 sigattn_paged_write(k, v, slots, self.k, self.v, self.workspace)
@@ -613,27 +616,17 @@ class PagedCache:
         """Undo the last reserve (none of its sequences, if the device refused
         it): the pages that it popped still stand above the stack's height."""
         before = self.lens - self.cu_seqlens.diff()
-        self.free_count += (self._pages(self.lens) - self._pages(before)).sum(dtype=torch.int32)
+        pages = lambda n: (n + self.page_size - 1) // self.page_size  # noqa: E731
+        self.free_count += (pages(self.lens) - pages(before)).sum(dtype=torch.int32)
         self.lens.copy_(before)
-
-    def _pages(self, lens):
-        return (lens + self.page_size - 1) // self.page_size
 
     def release(self, keep_lens=None) -> None:
         """Keep the first keep_lens[b] tokens of every sequence (None: none)
         and give the other pages back. If a sequence holds fewer than that, or
         the stack has no room for the pages, nothing changes and the error word
         is raised."""
-        height = self.free_count.clone()
         sigattn_paged_release(self.lens, keep_lens, self.block_table, self.free_pages, self.free_count, self.free_count,
-                              self.page_size, self.workspace)
-        # The lengths follow where the call was met: its rules once more.
-        keep = torch.zeros_like(self.lens) if keep_lens is None else keep_lens.reshape(self.lens.shape)
-        given = (self._pages(self.lens) - self._pages(keep)).sum()
-        most = self.block_table.shape[1] * self.page_size
-        met = ((keep >= 0) & (keep <= self.lens) & (self.lens <= most)).all()
-        met &= (height >= 0).all() & (height + given <= self.free_pages.numel()).all()
-        self.lens.copy_(torch.where(met, keep, self.lens))
+                              self.page_size, self.workspace, kv_lens_out=self.lens)
 
     def check(self) -> None:
         """Synchronise and raise if a call reported a problem on the device."""

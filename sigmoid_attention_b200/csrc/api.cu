@@ -585,6 +585,16 @@ int sigattn_paged_reserve(const int32_t* cached_lens, const int32_t* new_lens, i
                           int32_t* cu_seqlens, int32_t* kv_lens, int32_t* slots, int32_t* positions, int B,
                           int max_pages, int page_size, int num_pages, int rows, void* workspace,
                           size_t workspace_bytes, void* stream) {
+  return sigattn_paged_reserve_bounded(cached_lens, new_lens, block_table, free_pages, free_count, free_count_out,
+                                       cu_seqlens, kv_lens, slots, positions, B, max_pages, page_size, num_pages, rows,
+                                       INT_MAX, workspace, workspace_bytes, stream);
+}
+
+int sigattn_paged_reserve_bounded(const int32_t* cached_lens, const int32_t* new_lens, int32_t* block_table,
+                                  const int32_t* free_pages, const int32_t* free_count, int32_t* free_count_out,
+                                  int32_t* cu_seqlens, int32_t* kv_lens, int32_t* slots, int32_t* positions, int B,
+                                  int max_pages, int page_size, int num_pages, int rows, int max_new, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
   DeviceInfo info;
   int shift = 0;
   const void* words[] = {cached_lens, new_lens, block_table, free_pages, free_count, free_count_out, cu_seqlens, kv_lens};
@@ -592,13 +602,14 @@ int sigattn_paged_reserve(const int32_t* cached_lens, const int32_t* new_lens, i
   if (st != SIGATTN_OK) return st;
   for (const void* p : words)
     if (!aligned4(p)) return SIGATTN_ERR_INVALID_ARG;
-  if (rows < 0 || (rows > 0 && !aligned4(slots)) || (positions != nullptr && !aligned4(positions)))
+  if (rows < 0 || max_new < 0 || (rows > 0 && !aligned4(slots)) || (positions != nullptr && !aligned4(positions)))
     return SIGATTN_ERR_INVALID_ARG;
   if (rows > kMaxReserveRows) return SIGATTN_ERR_UNSUPPORTED;
   st = check_paged_call(workspace, workspace_bytes, kHeaderBytes, &info);
   if (st != SIGATTN_OK) return st;
   const PagedReserve a{cached_lens, new_lens, block_table, free_pages, free_count, free_count_out, cu_seqlens, kv_lens,
-                       slots, positions, B, max_pages, shift, num_pages, rows, static_cast<int*>(workspace)};
+                       slots, positions, B, max_pages, shift, num_pages, rows, max_new,
+                       static_cast<int*>(workspace)};
   return cuda_status(launch_paged_reserve(a, info.num_sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -606,17 +617,26 @@ int sigattn_paged_release(const int32_t* kv_lens, const int32_t* keep_lens, cons
                           int32_t* free_pages, const int32_t* free_count, int32_t* free_count_out, int B,
                           int max_pages, int page_size, int num_pages, void* workspace, size_t workspace_bytes,
                           void* stream) {
+  return sigattn_paged_release_lens(kv_lens, keep_lens, block_table, free_pages, free_count, free_count_out, nullptr, B,
+                                    max_pages, page_size, num_pages, workspace, workspace_bytes, stream);
+}
+
+int sigattn_paged_release_lens(const int32_t* kv_lens, const int32_t* keep_lens, const int32_t* block_table,
+                               int32_t* free_pages, const int32_t* free_count, int32_t* free_count_out,
+                               int32_t* kv_lens_out, int B, int max_pages, int page_size, int num_pages,
+                               void* workspace, size_t workspace_bytes, void* stream) {
   DeviceInfo info;
   int shift = 0;
   int st = check_pages(B, max_pages, page_size, num_pages, &shift);
   if (st != SIGATTN_OK) return st;
   if (!aligned4(kv_lens) || (keep_lens != nullptr && !aligned4(keep_lens)) || !aligned4(block_table) ||
-      !aligned4(free_pages) || !aligned4(free_count) || !aligned4(free_count_out))
+      !aligned4(free_pages) || !aligned4(free_count) || !aligned4(free_count_out) ||
+      (kv_lens_out != nullptr && !aligned4(kv_lens_out)))
     return SIGATTN_ERR_INVALID_ARG;
   st = check_paged_call(workspace, workspace_bytes, kHeaderBytes, &info);
   if (st != SIGATTN_OK) return st;
-  const PagedRelease a{kv_lens, keep_lens, block_table, free_pages, free_count, free_count_out, B, max_pages, shift,
-                       num_pages, static_cast<int*>(workspace)};
+  const PagedRelease a{kv_lens, keep_lens, block_table, free_pages, free_count, free_count_out, kv_lens_out, B,
+                       max_pages, shift, num_pages, static_cast<int*>(workspace)};
   return cuda_status(launch_paged_release(a, info.num_sms, static_cast<cudaStream_t>(stream)));
 }
 

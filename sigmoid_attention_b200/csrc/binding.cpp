@@ -83,8 +83,9 @@ struct Call {
     if (v < INT_MIN || v > INT_MAX) refuse("%s is out of range", name);
     return static_cast<int>(v);
   }
-  int integer(const char* name) {
-    const long long v = PyLong_AsLongLong(take());
+  int integer(const char* name) { return integer(take(), name); }
+  int integer(PyObject* o, const char* name) {
+    const long long v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) throw Refused{};
     return small(v, name);
   }
@@ -156,10 +157,12 @@ int reserve(Call& c) {
   int32_t* positions = Call::none(at_) ? nullptr : c.ints(at_, "positions", slots.numel());
   const int page = c.integer("page_size");
   const at::Tensor& ws = c.packed("workspace", at::kByte);
-  return unlocked(sigattn_paged_reserve, cached, fresh, table, static_cast<int32_t*>(pages.data_ptr()), count, count_out, cu, kv,
+  PyObject* bound = c.take();
+  const int max_new = Call::none(bound) ? INT_MAX : c.integer(bound, "max_new");
+  return unlocked(sigattn_paged_reserve_bounded, cached, fresh, table, static_cast<int32_t*>(pages.data_ptr()), count, count_out, cu, kv,
                                static_cast<int32_t*>(slots.data_ptr()), positions, Call::small(B, "B"), width, page,
                                Call::small(pages.numel(), "num_pages"), Call::small(slots.numel(), "rows"),
-                               ws.data_ptr(), ws.numel(), c.stream());
+                               max_new, ws.data_ptr(), ws.numel(), c.stream());
 }
 
 int release(Call& c) {
@@ -174,8 +177,10 @@ int release(Call& c) {
   int32_t* count_out = c.ints("free_count_out", 1);
   const int page = c.integer("page_size");
   const at::Tensor& ws = c.packed("workspace", at::kByte);
-  return unlocked(sigattn_paged_release, kv, keep_lens, table, static_cast<int32_t*>(pages.data_ptr()), count, count_out,
-                               Call::small(B, "B"), width, page, Call::small(pages.numel(), "num_pages"), ws.data_ptr(),
+  PyObject* after = c.take();
+  int32_t* kv_out = Call::none(after) ? nullptr : c.ints(after, "kv_lens_out", B);
+  return unlocked(sigattn_paged_release_lens, kv, keep_lens, table, static_cast<int32_t*>(pages.data_ptr()), count, count_out,
+                               kv_out, Call::small(B, "B"), width, page, Call::small(pages.numel(), "num_pages"), ws.data_ptr(),
                                ws.numel(), c.stream());
 }
 
@@ -261,7 +266,7 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef methods[] = {
-    method<reserve, 13>("paged_reserve"), method<release, 9>("paged_release"), method<write, 13>("paged_write"),
+    method<reserve, 14>("paged_reserve"), method<release, 10>("paged_release"), method<write, 13>("paged_write"),
     method<attend, 11>("fwd_paged"),      {nullptr, nullptr, 0, nullptr},
 };
 

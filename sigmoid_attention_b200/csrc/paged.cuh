@@ -17,6 +17,7 @@ struct PagedReserve {
   int* free_count_out;
   int *cu, *kv, *slots, *positions;
   int B, max_pages, page_shift, num_pages, rows;
+  int max_new;  // most new tokens of one sequence
   int* ws;
 };
 
@@ -26,6 +27,7 @@ struct PagedRelease {
   int* free_pages;
   const int* free_count;
   int* free_count_out;
+  int* kv_out;  // [B]; may be null
   int B, max_pages, page_shift, num_pages;
   int* ws;
 };

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(PagedReserve a) {
     const int c = a.cached[b], m = a.fresh[b];
     s_cached[b] = c;
     s_cu[b] = m;
-    if (c < 0 || m < 0 || c > most || m > most - c) {
+    if (c < 0 || m < 0 || c > most || m > most - c || m > a.max_new) {
       worst = min(worst, b);
     } else {
       tok += m;
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads) release_kernel(PagedRelease a) {
   grid_dep_launch();
   grid_dep_wait();
   extern __shared__ int smem_pages[];
-  __shared__ int s_bad, s_count;
+  __shared__ int s_bad, s_last, s_count;
   __shared__ float s_pages;
   int* s_pg = smem_pages;           // [B + 1] released pages before sequence b
   int* s_first = s_pg + a.B + 1;    // [B] the first page it gives back
@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(kThreads) release_kernel(PagedRelease a) {
   const int P = ok ? static_cast<int>(total) : 0;
   if (tid == 0) {
     if (!ok && blockIdx.x == 0) raise_invalid(a.ws, bad < a.B ? -(bad + 1) : 202);
-    if (last_reader(a.ws)) *a.free_count_out = count + P;
+    s_last = last_reader(a.ws);
+    if (s_last) *a.free_count_out = count + P;
     s_pg[a.B] = P;
   }
   for (int b = b0; b < b1; ++b) {
@@ -258,6 +259,8 @@ __global__ void __launch_bounds__(kThreads) release_kernel(PagedRelease a) {
     pg += gone;
   }
   __syncthreads();
+  if (s_last && a.kv_out != nullptr)
+    for (int b = tid; b < a.B; b += kThreads) a.kv_out[b] = !ok ? a.kv[b] : a.keep ? a.keep[b] : 0;
   for (int i = blockIdx.x * kThreads + tid; i < P; i += gridDim.x * kThreads) {
     const int b = owner(s_pg, a.B, i);
     int page = a.table[static_cast<size_t>(b) * a.max_pages + s_first[b] + i - s_pg[b]];

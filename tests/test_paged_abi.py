@@ -128,3 +128,23 @@ def test_binding_rejects_cpu_tensors_and_other_objects():
         sa.sigattn_paged_release(i, None, i.view(2, 1), i, i[:1], i[:1], 16, ws)
     with pytest.raises(ValueError, match="must be a tensor"):
         sa.sigattn_paged_release([1, 2], None, i.view(2, 1), i, i[:1], i[:1], 16, ws)
+
+
+@pytest.mark.parametrize("change, status", [(dict(max_new=-1), INVALID), (dict(slots=0), INVALID), (dict(page=24), UNSUPPORTED),
+                                            (dict(ws_bytes=255), INVALID)])
+def test_bounded_reserve_refusals(mem, change, status):
+    a = {**RESERVE, "max_new": 1, **change}
+    p = lambda v: None if v == 0 else mem[1] + (v - 1)  # noqa: E731
+    assert sa.library().sigattn_paged_reserve_bounded(
+        *(p(a[k]) for k in ("cached", "new", "table", "stack", "count", "count_out", "cu", "kv", "slots", "positions")),
+        a["B"], a["max_pages"], a["page"], a["num_pages"], a["rows"], a["max_new"], p(a["ws"]), a["ws_bytes"], None) == status
+
+
+@pytest.mark.parametrize("change, status", [(dict(kv_out=2), INVALID), (dict(kv=0), INVALID), (dict(B=4097), UNSUPPORTED),
+                                            (dict(ws=2), INVALID)])
+def test_release_lens_refusals(mem, change, status):
+    a = {**RELEASE, "kv_out": 1, **change}
+    p = lambda v: None if v == 0 else mem[1] + (v - 1)  # noqa: E731
+    assert sa.library().sigattn_paged_release_lens(
+        *(p(a[k]) for k in ("kv", "keep", "table", "stack", "count", "count_out", "kv_out")), a["B"], a["max_pages"],
+        a["page"], a["num_pages"], p(a["ws"]), a["ws_bytes"], None) == status

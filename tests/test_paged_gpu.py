@@ -1130,3 +1130,45 @@ def test_single_token_steps_of_a_cache_for_single_tokens():
     with pytest.raises(sa.SigattnError):
         cache.check()
     assert cache.lens.tolist() == [n] * B and bool((out == 0).all())
+
+
+@pytest.mark.parametrize("B", [3, 300, 4096])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_release_says_what_is_held(in_place, B):
+    """kv_lens_out after calls that are met and calls that are refused, of one and
+    of several CTAs."""
+    g = np.random.default_rng(B)
+    kv = g.integers(1, 12 * 16 + 1, B)
+    keep = g.integers(0, kv + 1)
+    table, stack = page_state(kv.tolist(), 16, 12, 2, B)
+    ws = workspace()
+    for what in ("kept", "none", "too many", "no room"):
+        f, s, lens = i32([3 if what == "no room" else 2]), i32(stack.tolist()), i32(kv.tolist())
+        out = lens if in_place else i32([-7] * B)
+        k = {"kept": keep, "none": None, "too many": np.where(np.arange(B) == B // 2, kv + 1, keep), "no room": None}[what]
+        sa.sigattn_paged_release(lens, None if k is None else i32(k.tolist()), i32(table.tolist()), s, f, f, 16, ws,
+                                 kv_lens_out=out)
+        want = {"kept": keep, "none": np.zeros_like(kv)}.get(what, kv)
+        assert out.tolist() == want.tolist() and (in_place or lens.tolist() == kv.tolist())
+        status = sa.sigattn_read_error(ws)
+        assert status == {"too many": (1, -(B // 2 + 1)), "no room": (1, 202)}.get(what, (0, 0))
+        assert (int(f) > 3) == (status == (0, 0)) or what == "kept"
+
+
+@pytest.mark.parametrize("B", [3, 300, 4096])
+def test_reserve_bounds_new_tokens(B):
+    """max_new met by the largest, and one below it."""
+    new = [1 + 7 * i % 20 for i in range(B)]
+    new[B // 2] = 21
+    table, stack = page_state([5] * B, 16, 3, 2 * B, B)
+    for max_new in (21, 20, None):
+        ws, e = workspace(), lambda n: torch.full((n,), -77, dtype=torch.int32, device=DEV)  # noqa: E731
+        t, count, cu, kv, slots = i32(table.tolist()), e(1), e(B + 1), e(B), e(sum(new))
+        sa.sigattn_paged_reserve(i32([5] * B), i32(new), t, i32(stack.tolist()), i32([2 * B]), count, cu, kv, slots, None, 16, ws,
+                                 max_new=max_new)
+        if max_new == 20:
+            assert sa.sigattn_read_error(ws) == (1, -(B // 2 + 1))
+            assert kv.tolist() == [5] * B and int(count) == 2 * B and t.tolist() == table.tolist() and bool((slots == -1).all())
+        else:
+            assert sa.sigattn_read_error(ws) == (0, 0)
+            assert kv.tolist() == [5 + m for m in new] and bool((slots >= 0).all())
