@@ -360,9 +360,9 @@ SIGATTN_API size_t sigattn_paged_workspace_size(int Hq, int Hkv, int d, int max_
  * position p = kv_lens[b] - q_b + i of its sequence and sees N keys: the first
  * p + 1 with `causal`, else all kv_lens[b];
  *     o_i = sum_{j < N} sigma(q_i . k_j / sqrt(d) - ln N) v_j.
- * The bias counts the keys that the row sees, so a causal row's result does
- * not depend on how its prompt was cut into chunks, and with causal = 0 and
- * nothing cached before it is sigattn_fwd_varlen's. A row that sees no key
+ * The bias counts the keys that the row sees, so but for rounding a causal
+ * row's result does not depend on how its prompt was cut into chunks, and with
+ * causal = 0 and nothing cached before it is sigattn_fwd_varlen's. A row that sees no key
  * (kv_lens[b] = 0, or p < 0 where more rows than tokens are given) is zero.
  *  - q: `total` rows of [Hq][d]; o: [total][Hq][d] bf16, contiguous. Rows
  *    outside every [cu_seqlens[b], cu_seqlens[b+1]) are never written.
@@ -381,7 +381,14 @@ SIGATTN_API size_t sigattn_paged_workspace_size(int Hq, int Hkv, int d, int max_
  *  - The keys are cut over the SMs where that balances the work, and the
  *    fp32 partial sums are added in a fixed order: no atomics touch a result,
  *    and a repeated call gives the same bits.
- *  - Arithmetic as sigattn_fwd. One launch. Forward only. */
+ *  - Arithmetic: operands, sums and roundings as sigattn_fwd (weights are
+ *    rounded to bf16 before the second product); sigma itself is taken by an
+ *    exponential and a reciprocal, or in the many-row kernel's far tail by a
+ *    cubic. Hq / Hkv * max_seqlen_q (<= 64 at d = 64, <= 32 at d = 128, or more)
+ *    decides between two kernels, and the batch decides where keys are cut, so
+ *    the last bits of a row may differ with max_seqlen_q and with the other
+ *    sequences of its batch.
+ *  - One launch. Forward only. */
 SIGATTN_API int sigattn_fwd_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, void* o,
                                   const int32_t* cu_seqlens, const int32_t* kv_lens, const int32_t* block_table, int B,
                                   int Hq, int Hkv, int max_seqlen_q, int total, int max_pages, int page_size,

@@ -35,8 +35,8 @@
 //    took 4200 cycles per segment before, most of them this chain.
 //
 // Bound by HBM: 64 texts of 256 to 8192 tokens, 32 query heads on 8, d = 128,
-// 16-token pages: 114 us, 6.3 TB/s of 6.57 (a copy's rate); four texts of 100 to 262
-// thousand tokens 187 us, 6.8 TB/s. Short calls are bound by latency: one token over
+// 16-token pages: 116 us, 6.2 TB/s of 6.57 (a copy's rate); four texts of 100 to 262
+// thousand tokens 189 us, 6.7 TB/s. Short calls are bound by latency: one token over
 // 1000 keys 7.7 us, of which 2.6 lie before the first load (lengths, then pages,
 // then the load, each a trip to memory) and 2 after the last product (parts
 // stored, counted, added up).

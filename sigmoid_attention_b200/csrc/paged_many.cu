@@ -28,11 +28,11 @@
 // What bounds it: the chain of a tile's block, S, weights, PV. With two tiles in turn
 // a block of both takes 4280 cycles, of which the weights' passes, one after the
 // other, are 3500 (1024 each if the 16 MUFU lanes never waited); the tensor pipe is
-// busy for 41 % of a call of two 4096-token prompts; on long calls the clock is held down by power besides. Two
-// prompts of 4000 tokens behind 8192 to 16384 (16 heads of 128): 880 us, 925 TFLOPS;
-// 4096-token prompts, not causal: 543 us, 1010 TFLOPS. Short calls wait for their
-// start (9000 cycles to the first load, half of them instruction misses) and for
-// cut tiles' parts.
+// busy for 41 % of a call of two 4096-token prompts. On long calls the clock is held
+// down by power besides. Two prompts of 4000 tokens behind 8192 to 16384 (16 heads of
+// 128): 840 to 1025 us, 970 to 795 TFLOPS; 4096-token prompts, not causal: 543 us,
+// 1010 TFLOPS. Short calls wait for their start (9000 cycles to the first load, half
+// of them instruction misses) and for cut tiles' parts.
 //
 // Roles (20 warps): 0-15 epilogue (warps 0-7 tile 0, 8-15 tile 1; per tile, four
 // warps for every other 32 of a block's keys), 16 and 17 the producers of K and
