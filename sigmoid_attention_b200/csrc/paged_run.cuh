@@ -346,7 +346,7 @@ struct RunWalker {
       bool works = x.m > 0 && seq_base + lane < a.B;
       int upto = x.m > 0 ? x.start + x.m : 0;
       if (__builtin_expect(reach >= 0, 0)) {  // a bad sequence somewhere: none may start before an earlier one's end
-#pragma unroll 1
+#pragma unroll
         for (int o = 1; o < 32; o <<= 1) upto = max(upto, __shfl_up_sync(0xffffffffu, upto, o));
         const int before = __shfl_up_sync(0xffffffffu, upto, 1);
         works &= x.start >= (lane > 0 ? max(before, reach) : reach);

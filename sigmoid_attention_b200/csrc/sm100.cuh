@@ -48,7 +48,11 @@ __device__ __forceinline__ unsigned long long error_word(int code, int site) {
   return static_cast<unsigned long long>(static_cast<uint32_t>(site)) << 32 | static_cast<uint32_t>(code);
 }
 __device__ __forceinline__ void raise_invalid(int* ws, int site) {
-  atomicCAS(reinterpret_cast<unsigned long long*>(ws), 0ull, error_word(1 /* SIGATTN_ERR_INVALID_ARG */, site));
+  unsigned long long seen = 0, want;
+  do {  // (a caller may have cleared the code alone)
+    want = seen;
+    seen = atomicCAS(reinterpret_cast<unsigned long long*>(ws), want, error_word(1 /* SIGATTN_ERR_INVALID_ARG */, site));
+  } while (seen != want && static_cast<uint32_t>(seen) == 0);
 }
 __device__ __forceinline__ void raise_timeout(int* ws, int site) {
   atomicExch(reinterpret_cast<unsigned long long*>(ws), error_word(4 /* SIGATTN_ERR_TIMEOUT */, site));

@@ -1172,3 +1172,13 @@ def test_reserve_bounds_new_tokens(B):
         else:
             assert sa.sigattn_read_error(ws) == (0, 0)
             assert kv.tolist() == [5 + m for m in new] and bool((slots >= 0).all())
+
+
+@pytest.mark.parametrize("mild", MILD)
+def test_error_after_the_word_alone_was_cleared(mild):
+    """Word 0 is the status: a caller may clear it without the site beside it."""
+    fails, what = MILD[mild]
+    ws = workspace(1024)
+    ws.view(torch.int32)[1] = 77
+    fails(ws)
+    assert sa.sigattn_read_error(ws) == what
