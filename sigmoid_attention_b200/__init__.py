@@ -562,7 +562,9 @@ class PagedCache:
     included), stores them and attends; ``release`` takes tokens back or ends
     sequences. Nothing synchronises, so a step can be captured into a CUDA
     graph (make one call outside the capture first); ``check`` reads the sticky
-    error word."""
+    error word. ``max_new`` bounds the new tokens of one sequence in a step and
+    with them chooses the attention kernel: where Hq / Hkv * max_new is over 64
+    (d = 64) or 32 (d = 128), single tokens take the one for many rows too."""
 
     def __init__(self, num_pages: int, page_size: int, Hq: int, Hkv: int, d: int, batch: int, max_pages: int,
                  max_new: int = 1, device=None):
